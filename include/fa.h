@@ -226,6 +226,14 @@ typedef struct {
    * a group over several thread blocks, each writes its own fp32 partial sums
    * and they are added in a fixed order). */
   int heads_kv;
+  /* Sliding window with visible first tokens (causal calls only): with
+   * window > 0, query i attends key j iff it does without the window and
+   * j > i + Nk_b - Nq_b - window (the window's keys end at the query's own
+   * position) or j < sinks (the first tokens of the sequence stay visible).
+   * K/V tiles that no query of a tile sees are neither loaded nor computed.
+   * 0: no window (sinks is then ignored).  Negative values, or a window
+   * without causal, return FA_ERR_INVALID_ARG. */
+  int window, sinks;
 } fa_attention_desc_t;
 
 /* Forward pass for a general layout.  LSE is fp32 [B, H, seqlen_q]

@@ -97,6 +97,7 @@ class AttentionDesc(ctypes.Structure):
         ("dq", Strides), ("dk", Strides), ("dv", Strides),
         ("dropout_row0", ctypes.c_int64), ("dropout_key0", ctypes.c_int64),
         ("heads_kv", ctypes.c_int),
+        ("window", ctypes.c_int), ("sinks", ctypes.c_int),
     ]
 
 
@@ -352,7 +353,8 @@ _Q_SIDE = ("q", "o", "dout", "dq")
 
 
 def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
-          seqlens_k, dropout_p, seed, block_mask, tensors, dropout_pos=(0, 0)):
+          seqlens_k, dropout_p, seed, block_mask, tensors, dropout_pos=(0, 0), window=0,
+          sinks=0):
     import torch
     if layout not in ("bhsd", "bshd", "thd"):
         raise ValueError(f"unknown layout {layout!r}")
@@ -399,16 +401,26 @@ def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, 
     a.dropout_p = float(dropout_p)
     a.seed = int(seed) & 0xFFFFFFFFFFFFFFFF
     a.dropout_row0, a.dropout_key0 = (int(x) for x in dropout_pos)
+    a.window, a.sinks = _window(window, sinks)
     for name, t in tensors.items():
         setattr(a, name, _strides(t, layout))
     return a, keep
+
+
+def _window(window, sinks):
+    """(window, sinks) as C ints; past 2^31 - 1 a window hides nothing (the
+    library takes one as long as the keys for none)."""
+    window, sinks = int(window or 0), int(sinks or 0)
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    return min(window, 2**31 - 1), min(sinks, 2**31 - 1)
 
 
 @_nvtx("fa.forward_general")
 def forward_general(q, k, v, *, layout="bhsd", cu_seqlens_q=None, cu_seqlens_k=None,
                     max_seqlen_q=None, max_seqlen_k=None, scale=None, causal=False,
                     seqlens_k=None, dropout_p=0.0, seed=0, block_mask=None, out=None, lse=None,
-                    dropout_row0=0, dropout_key0=0):
+                    dropout_row0=0, dropout_key0=0, window=0, sinks=0):
     """O, LSE for a general layout (fa_fwd_ex).
 
     layout "bhsd": q [B, H, N_q, d], k / v [B, H, N_k, d]; "bshd": q [B, N_q, H, d],
@@ -421,13 +433,15 @@ def forward_general(q, k, v, *, layout="bhsd", cu_seqlens_q=None, cu_seqlens_k=N
     dropout_row0 / dropout_key0: positions of the call's first query row and
     first key in the sequence the dropout bits are keyed by (a block of a
     longer sequence); the key position a multiple of 8.
+    window (with causal): each query sees the last `window` keys up to its own
+    position and the first `sinks` keys of its sequence; 0 or None: all keys.
     """
     import torch
     if out is None:
         out = torch.empty_like(q)
     a, keep = _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale,
                     causal, seqlens_k, dropout_p, seed, block_mask,
-                    dict(q=q, k=k, v=v, o=out), (dropout_row0, dropout_key0))
+                    dict(q=q, k=k, v=v, o=out), (dropout_row0, dropout_key0), window, sinks)
     if lse is None:
         lse = torch.empty(_lse_shape(q, layout), dtype=torch.float32, device=q.device)
     _check_lse(lse, q, layout)
@@ -460,7 +474,8 @@ def general_workspace_size(q, k, **kw):
                     kw.get("cu_seqlens_k"), kw.get("max_seqlen_q"), kw.get("max_seqlen_k"),
                     kw.get("scale"), kw.get("causal", False), kw.get("seqlens_k"),
                     kw.get("dropout_p", 0.0), kw.get("seed", 0), kw.get("block_mask"),
-                    dict(q=q, k=k, v=k, o=q, dout=q, dq=q, dk=k, dv=k))
+                    dict(q=q, k=k, v=k, o=q, dout=q, dq=q, dk=k, dv=k),
+                    window=kw.get("window", 0), sinks=kw.get("sinks", 0))
     return int(library().fa_bwd_ex_workspace_size(ctypes.byref(a)))
 
 
@@ -468,7 +483,8 @@ def general_workspace_size(q, k, **kw):
 def backward_general(q, k, v, o, lse, dout, *, layout="bhsd", cu_seqlens_q=None,
                      cu_seqlens_k=None, max_seqlen_q=None, max_seqlen_k=None, scale=None,
                      causal=False, seqlens_k=None, dropout_p=0.0, seed=0, block_mask=None,
-                     workspace=None, dq=None, dk=None, dv=None, dropout_row0=0, dropout_key0=0):
+                     workspace=None, dq=None, dk=None, dv=None, dropout_row0=0, dropout_key0=0,
+                     window=0, sinks=0):
     """dQ, dK, dV for a general layout (fa_bwd_ex); arguments as forward_general."""
     import torch
     dq = torch.empty_like(q) if dq is None else dq
@@ -477,7 +493,7 @@ def backward_general(q, k, v, o, lse, dout, *, layout="bhsd", cu_seqlens_q=None,
     a, keep = _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale,
                     causal, seqlens_k, dropout_p, seed, block_mask,
                     dict(q=q, k=k, v=v, o=o, dout=dout, dq=dq, dk=dk, dv=dv),
-                    (dropout_row0, dropout_key0))
+                    (dropout_row0, dropout_key0), window, sinks)
     _check_lse(lse, q, layout)
     lib = library()
     need = int(lib.fa_bwd_ex_workspace_size(ctypes.byref(a)))

@@ -80,6 +80,7 @@ struct Problem {
   fa_strides_t q, k, v, o, dout, dq, dk, dv;
   int64_t drop_row0, drop_key0;  // dropout positions of the first query row and key
   int Hkv;                       // K / V heads (H / Hkv query heads share each)
+  int window, sinks;             // sliding window (0: none), first keys that stay visible
 
   int rows_q() const { return packed ? total_q : nq; }
   int rows_k() const { return packed ? total_k : nk; }
@@ -141,6 +142,12 @@ fa_status_t resolve(const fa_attention_desc_t* a, Problem* p, Uses uses) {
   if (a->dropout_row0 < 0 || a->dropout_key0 < 0 || a->dropout_key0 % 8 != 0 ||
       a->dropout_row0 > 0x7FFFFFFFll - a->seqlen_q || a->dropout_key0 > 0x7FFFFFFFll - a->seqlen_k)
     return FA_ERR_INVALID_ARG;
+  if (a->window < 0 || a->sinks < 0 || (a->window > 0 && a->causal == 0)) return FA_ERR_INVALID_ARG;
+  // a window as long as the keys hides nothing: the kernels without it run.
+  // Positions are below kMaxRows, so longer windows and more first keys than
+  // that change nothing either (and the kernels' sums stay inside 32 bits).
+  p->window = a->window < a->seqlen_k ? a->window : 0;
+  p->sinks = a->sinks < kMaxRows ? a->sinks : kMaxRows;
   p->drop_row0 = a->dropout_row0;
   p->drop_key0 = a->dropout_key0;
   p->Hkv = hkv;
@@ -347,6 +354,8 @@ fa_status_t run_fwd(const Problem& pr, const void* q, const void* k, const void*
   p.B = pr.B;
   p.H = pr.H;
   p.group = pr.H / pr.Hkv;
+  p.window = pr.window;
+  p.sinks = pr.sinks;
   p.d_real = pr.d;
   p.scale_log2 = static_cast<float>(static_cast<double>(pr.scale) * kLog2e);
   p.causal = pr.causal;
@@ -406,6 +415,8 @@ fa_status_t bwd_params(fa::BwdParams* p, const Problem& pr, const void* workspac
   p->B = pr.B;
   p->H = pr.H;
   p->group = pr.H / pr.Hkv;
+  p->window = pr.window;
+  p->sinks = pr.sinks;
   p->d_real = pr.d;
   p->scale = pr.scale;
   p->scale_log2 = static_cast<float>(static_cast<double>(pr.scale) * kLog2e);

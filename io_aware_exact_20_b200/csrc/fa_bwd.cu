@@ -360,7 +360,10 @@ __global__ void __launch_bounds__(256) bwd_kv_post_kernel(const BwdParams p) {
 // counters' row / key offsets (as the forward's POS instances); the others
 // see one query head per K / V head and zero offsets at compile time.  Built
 // only with the direct mask walk.
-template <int D, bool DROPOUT, bool BITS, bool GEN = false>
+// WIN (general instances): sliding window.  Key j is seen by query i only if
+// i + off < j + window or j < sinks, so a key tile past the first `sinks` keys
+// ends its walk at the query tile of its last key's last query.
+template <int D, bool DROPOUT, bool BITS, bool GEN = false, bool WIN = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -424,6 +427,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     w.qb_begin = lo <= 0 ? 0 : lo / 128;
   } else {
     w.qb_begin = 0;
+  }
+  if constexpr (WIN) {
+    if (w.kb * 128 >= p.sinks) {
+      const int last = w.kb * 128 + 127 + p.window - 1 - w.off;  // last query that sees a key here
+      w.nqb = last < 0 ? 0 : min(w.nqb, last / 128 + 1);
+    }
   }
   w.nbk = p.nbk;
   w.bm = p.block_mask;
@@ -906,10 +915,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // causal: query q of this tile sees this thread's key iff q >= qmin
       const bool diag = w.causal && (w.kb * 128 + 127 > qb * 128 + w.off);
       const int qmin = j + (w.kb - qb) * 128 - w.off;
-      // only the diagonal tile of a causal mask and padding keys need masking;
-      // the choice must be warp-uniform (the TMEM loads and stores in both
-      // versions are warp-collective)
-      const bool masked = __any_sync(0xffffffffu, diag || !key_live);
+      // window: query q of this tile sees this thread's key iff q < qmax
+      int qmax = 0x7FFFFFFF;
+      if constexpr (WIN)
+        if (jg >= p.sinks) qmax = jg + p.window - w.off - qb * 128;
+      // only the diagonal tile of a causal mask, the last tiles of a window and
+      // padding keys need masking; the choice must be warp-uniform (the TMEM
+      // loads and stores in both versions are warp-collective)
+      const bool masked = __any_sync(0xffffffffu, diag || !key_live || (WIN && qmax < 128));
 
       // P for queries qoff + 4 k4 + [0, 4) of this key: exp2(S^T scale log2e - LSE log2e)
       auto p_quad = [&](auto mask_tag, const uint32_t* sv, int qoff, int k4, float pv[4]) {
@@ -926,7 +939,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if constexpr (MASKED) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!key_live || (diag && qoff + 4 * k4 + e < qmin)) pv[e] = 0.f;
+            if (!key_live || (diag && qoff + 4 * k4 + e < qmin) ||
+                (WIN && qoff + 4 * k4 + e >= qmax))
+              pv[e] = 0.f;
         }
       };
       // keep bit of query qoff + 4 k4 + e (= 8 g + r, g = k4 / 2, r = 4 (k4 % 2) + e)
@@ -1276,13 +1291,13 @@ cudaError_t launch_pre_t(const BwdParams& p, cudaStream_t stream) {
   return launch_overlapped(bwd_pre_kernel<D>, prepost_grid<D>(p), dim3(256), 0, stream, p);
 }
 
-template <int D, bool DROPOUT, bool BITS, bool GEN = false>
+template <int D, bool DROPOUT, bool BITS, bool GEN = false, bool WIN = false>
 cudaError_t launch_main_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tdo, const CUtensorMap& tdq, const BwdParams& p,
                           cudaStream_t stream) {
   using L = BwdLayout<D>;
   static_assert(!BITS || L::BIT_WORDS > 0, "no bitmask at this head dim");
-  auto kern = bwd_main_kernel<D, DROPOUT, BITS, GEN>;
+  auto kern = bwd_main_kernel<D, DROPOUT, BITS, GEN, WIN>;
   // The setmaxnreg split (d = 128) is sized for exactly 128 registers per
   // thread at launch; with any other count an increase could wait forever.
   static OncePerContext prepared;
@@ -1322,6 +1337,18 @@ cudaError_t launch_bwd_pre(int d, const BwdParams& p, cudaStream_t stream) {
 cudaError_t launch_bwd_main(int d, bool dropout, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const CUtensorMap& tdo, const CUtensorMap& tdq,
                             const BwdParams& p, cudaStream_t stream) {
+  if (p.window > 0) {
+    if (d == 64)
+      return dropout ? launch_main_t<64, true, false, true, true>(tq, tk, tv, tdo, tdq, p, stream)
+                     : launch_main_t<64, false, false, true, true>(tq, tk, tv, tdo, tdq, p, stream);
+    if (d == 128)
+      return dropout ? launch_main_t<128, true, false, true, true>(tq, tk, tv, tdo, tdq, p, stream)
+                     : launch_main_t<128, false, false, true, true>(tq, tk, tv, tdo, tdq, p, stream);
+    if (d == 256)
+      return dropout ? launch_main_t<256, true, false, true, true>(tq, tk, tv, tdo, tdq, p, stream)
+                     : launch_main_t<256, false, false, true, true>(tq, tk, tv, tdo, tdq, p, stream);
+    return cudaErrorInvalidValue;
+  }
   // grouped K / V heads, or dropout on a block of a longer sequence
   if (p.group > 1 || (dropout && (p.drop_row0 != 0u || p.drop_kgrp0 != 0u))) {
     if (d == 64)

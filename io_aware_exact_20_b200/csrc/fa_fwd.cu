@@ -147,10 +147,15 @@ struct FwdLayout {
 // one.  kRows bitmask rows (one per Q tile) of kWpr words each; kernels
 // launched without a block mask, or with rows longer than the bitmask, are
 // built without it (kBits false) and test the mask's bytes directly.
-template <int kRows, int kWpr, bool kBits>
+// Sliding window (kWin): row i also needs j > i + off - win or j < sinks.  The
+// K/V tiles of a Q tile are then the ones that hold the first `sinks` keys and
+// the ones from win_kb, the tile of the oldest key its first row sees; next()
+// jumps from the former to the latter.
+template <int kRows, int kWpr, bool kBits, bool kWin>
 struct FwdWork {
   int b, h, bh, q0, qb0, lq, kv_len, n_kb, kb_end, nbk, off, qrow, krow, tb;
   bool exists1, causal;
+  int win, sinks, win_kb;  // kWin only
   const uint8_t* bm;
   const uint32_t* bits;  // shared-memory bitmask rows, or null
 #ifdef FA_DEBUG_BOUNDS
@@ -164,6 +169,7 @@ struct FwdWork {
     if (t == 1 && !exists1) return false;
     if (kb >= n_kb) return false;
     if (causal && kb * 128 > last_row(t) + off) return false;
+    if (kWin && kb * 128 >= sinks && kb * 128 + 127 <= q0 + 128 * t + off - win) return false;
     if (bm != nullptr && (!FA_IN_BOUNDS(status, static_cast<long long>(qb0 + t) * nbk + kb, 1,
                                         ext_mask) ||
                           bm[static_cast<size_t>(qb0 + t) * nbk + kb] == 0))
@@ -192,6 +198,7 @@ struct FwdWork {
       }
       return kb_end;
     }
+    if (kWin && kb < win_kb && kb * 128 >= sinks) kb = min(win_kb, kb_end);
     while (kb < kb_end && !any(kb)) ++kb;
     return kb;
   }
@@ -205,8 +212,9 @@ __device__ __forceinline__ void named_bar_sync() {
 
 // POS: the dropout counter is offset by the call's row / key positions in a
 // longer sequence (instantiated only with dropout and the direct mask walk; the
-// other instances see compile-time zeros).
-template <int D, bool DROPOUT, bool BITS, bool POS = false>
+// other instances see compile-time zeros).  WIN: sliding window (with the
+// direct mask walk, and dropout through POS).
+template <int D, bool DROPOUT, bool BITS, bool POS = false, bool WIN = false>
 __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  FwdWork<NQ, L::BIT_WORDS / NQ, BITS> w;
+  FwdWork<NQ, L::BIT_WORDS / NQ, BITS, WIN> w;
   {
     const int nqp = (p.rows.nq + 128 * NQ - 1) / (128 * NQ);
     int tile = 0;
@@ -260,6 +268,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
       w.kb_end = last < 0 ? 0 : min(w.n_kb, last / 128 + 1);
     } else {
       w.kb_end = w.n_kb;
+    }
+    if constexpr (WIN) {
+      w.win = p.window;
+      w.sinks = p.sinks;
+      w.win_kb = max(0, w.q0 + w.off - p.window + 1) / 128;
     }
     w.nbk = p.nbk;
     w.bm = p.block_mask;
@@ -582,8 +595,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
         const int j0 = kb * 128 + KW * hp;  // first key of this block
         // masking is needed where a key of this block lies past the first
         // row's causal limit, or past the key length
-        const bool need_mask =
+        bool need_mask =
             (w.causal && j0 + KW - 1 > w.q0 + 128 * t + w.off) || (j0 + KW > w.kv_len);
+        // ... or before the last row's window, unless all are first keys
+        if constexpr (WIN)
+          need_mask = need_mask ||
+                      (j0 <= w.q0 + 128 * t + 127 + w.off - w.win && j0 + KW > w.sinks);
         // row maximum with independent partial maxima (short dependency chains;
         // as many as the register budget allows), two scores per max instruction
         constexpr int kParts = C::MAX_PARTS;
@@ -592,9 +609,16 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
         for (int u = 0; u < kParts; ++u) mxp[u] = -INFINITY;
         if (need_mask) {
           const int lim = w.causal ? min(w.kv_len - j0, i + w.off - j0 + 1) : (w.kv_len - j0);
+          if constexpr (WIN) {
+            const int lo = i + w.off - w.win + 1 - j0, first = w.sinks - j0;
 #pragma unroll
-          for (int j = 0; j < KW; ++j)
-            if (j >= lim) sr[j] = __float_as_uint(-INFINITY);
+            for (int j = 0; j < KW; ++j)
+              if (j >= lim || (j < lo && j >= first)) sr[j] = __float_as_uint(-INFINITY);
+          } else {
+#pragma unroll
+            for (int j = 0; j < KW; ++j)
+              if (j >= lim) sr[j] = __float_as_uint(-INFINITY);
+          }
         }
 #pragma unroll
         for (int c = 0; c < KW / 2; ++c)
@@ -801,12 +825,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
   }
 }
 
-template <int D, bool DROPOUT, bool BITS, bool POS = false>
+template <int D, bool DROPOUT, bool BITS, bool POS = false, bool WIN = false>
 cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const FwdParams& p, cudaStream_t stream) {
   using L = FwdLayout<D>;
   using C = FwdCfg<D>;
-  auto kern = fwd_kernel<D, DROPOUT, BITS, POS>;
+  auto kern = fwd_kernel<D, DROPOUT, BITS, POS, WIN>;
   // The setmaxnreg split is sized for exactly LAUNCH_REGS registers per thread
   // at launch; with any other count an increase could wait forever.  Checked,
   // with the shared-memory attribute set, once per device and context.
@@ -840,6 +864,18 @@ bool uses_bits(const FwdParams& p) {
 
 cudaError_t launch_fwd(int d, bool dropout, const CUtensorMap& tq, const CUtensorMap& tk,
                        const CUtensorMap& tv, const FwdParams& p, cudaStream_t stream) {
+  if (p.window > 0) {
+    if (d == 64)
+      return dropout ? launch_fwd_t<64, true, false, true, true>(tq, tk, tv, p, stream)
+                     : launch_fwd_t<64, false, false, false, true>(tq, tk, tv, p, stream);
+    if (d == 128)
+      return dropout ? launch_fwd_t<128, true, false, true, true>(tq, tk, tv, p, stream)
+                     : launch_fwd_t<128, false, false, false, true>(tq, tk, tv, p, stream);
+    if (d == 256)
+      return dropout ? launch_fwd_t<256, true, false, true, true>(tq, tk, tv, p, stream)
+                     : launch_fwd_t<256, false, false, false, true>(tq, tk, tv, p, stream);
+    return cudaErrorInvalidValue;
+  }
   if (dropout && (p.drop_row0 != 0u || p.drop_kgrp0 != 0u)) {  // a block of a longer sequence
     if (d == 64) return launch_fwd_t<64, true, false, true>(tq, tk, tv, p, stream);
     if (d == 128) return launch_fwd_t<128, true, false, true>(tq, tk, tv, p, stream);

@@ -171,6 +171,7 @@ struct FwdParams {
   uint64_t timeout_ns;
   int mask_bitmap;            // block masks: 1 = walk them through a shared-memory bitmask
   int group;                  // query heads per K / V head (1 = one K / V head each)
+  int window, sinks;          // sliding window (0: none) and first keys that stay visible
 #ifdef FA_DEBUG_BOUNDS
   Extents ext;
 #endif
@@ -218,6 +219,7 @@ struct BwdParams {
                               // query heads [p, p + 1) * group / split of the group and
                               // writing its dK / dV to slice p of ws_dk / ws_dv
   int rows_tb;                // batch coordinates of the tensors (B padded, 1 packed)
+  int window, sinks;          // as in FwdParams
   // fp32 dK / dV slices [split][rows_tb][H_kv][key rows][D] when split > 1
   float* ws_dk;
   float* ws_dv;
