@@ -305,6 +305,115 @@ fa_status_t fa_convert_f32_bf16(void* out, const float* in, int64_t n, void* str
 fa_status_t fa_qkv_projection(const void* x, const void* w, const void* bias, void* q, void* k,
                               void* v, int B, int N, int H, int d, int d_model, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key / value cache: decode attention and the cache's pages
+ * ------------------------------------------------------------------------
+ * Serving keeps the keys and values of every sequence in pages of a common
+ * pool.  A cache has `slots` sequences; slot s holds lengths[s] tokens, token
+ * j of it in row j % page_size of page table[s][j / page_size].  A page may be
+ * held by several slots (they forked from one another); refs[p] counts them
+ * and 0 means free.  Table cells without a page hold -1.
+ *
+ * k, v: bf16, [layers][pages][heads_kv][page_size][d] views with d contiguous:
+ * element strides of a layer (k_layer, v_layer) and of a page, a head and a
+ * row (ks, vs; their `batch` is the page stride), all non-negative multiples
+ * of 8, 16-byte aligned bases.  d as in the attention calls.  table int32
+ * [slots][max_pages], lengths int32 [slots], refs int32 [pages], contiguous
+ * device memory; refs may be NULL for the calls that only read or write rows
+ * (fa_cache_write, fa_cache_attend).  max_pages <= 2^20, max_pages * page_size
+ * <= 2^30.
+ *
+ * The calls are asynchronous on `stream`, allocate nothing and can be captured:
+ * lengths, page numbers, free pages and the copies to make are all found on
+ * the device.  They check these against the sizes given here: a slot outside
+ * [0, slots) is skipped, a page outside [0, pages) holds no keys, a length
+ * outside [0, max_pages * page_size] is cut to it.  Calls that change the same
+ * cache are ordered by the caller (one stream, or events).  Workspaces:
+ * fa_cache_workspace_size(cache, n) bytes, 256-byte aligned, contents
+ * irrelevant, not shared by calls that may overlap. */
+typedef struct {
+  int layers, pages, page_size, heads_kv, head_dim;
+  int slots, max_pages;
+  void* k;
+  void* v;
+  int64_t k_layer, v_layer;
+  fa_strides_t ks, vs;
+  int32_t* table;
+  int32_t* lengths;
+  int32_t* refs;
+} fa_cache_t;
+
+/* Workspace of fa_cache_extend, fa_cache_fork, fa_cache_copy_pages (n: their
+ * entries) and fa_cache_compact (n ignored).  0 if the description is invalid. */
+size_t fa_cache_workspace_size(const fa_cache_t* cache, int n);
+
+/* Grows slots[i] by tokens[i] >= 0 tokens, i < n: takes pages for the new
+ * positions, the free ones with the lowest numbers first in the order of i,
+ * and, where the last page is partly filled and held by another slot too,
+ * replaces it by a page of its own with the filled rows copied (all layers).
+ * Sets lengths and writes start[i], the first new position, for
+ * fa_cache_write.  start[i] = -1 and nothing of the slot changes where an entry
+ * cannot be granted: slot out of range or named by an earlier entry, negative
+ * tokens, more than max_pages pages, or (for entries that need pages) not
+ * enough free pages for it and all entries before it. */
+fa_status_t fa_cache_extend(const fa_cache_t* cache, const int32_t* slots, const int32_t* tokens,
+                            int n, int32_t* start, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Writes keys and values of one layer: entry i's rows to positions start[i],
+ * start[i] + 1, ... of slots[i]; start[i] < 0: nothing.  k, v: bf16
+ * [total][heads_kv][d] with element strides of a row and a head (multiples of
+ * 8).  cu NULL: one row per entry (total = n); else int32 [n + 1] offsets, rows
+ * cu[i] .. cu[i+1]-1.  A position outside the slot's table or without a page is
+ * skipped. */
+fa_status_t fa_cache_write(const fa_cache_t* cache, int layer, const void* k, const void* v,
+                           int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
+                           const int32_t* slots, const int32_t* start, const int32_t* cu, int n,
+                           int total, void* stream);
+
+/* Slot dst[i] lets its pages go and takes src[i]'s pages and length, i < n; all
+ * sources are read before any destination is replaced, so beams can be
+ * permuted in one call.  An entry with src[i] == dst[i], a slot out of range
+ * or the destination of an earlier entry is skipped. */
+fa_status_t fa_cache_fork(const fa_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The slots let their pages go: refs counted down, table cells -1, length 0. */
+fa_status_t fa_cache_free(const fa_cache_t* cache, const int32_t* slots, int n, void* stream);
+
+/* Packs the pages in use into the lowest numbers: with U pages in use, the k-th
+ * used page from U on moves into the k-th free page below U (all layers,
+ * whole pages); table and refs follow.  used: device int32, receives U. */
+fa_status_t fa_cache_compact(const fa_cache_t* cache, int32_t* used, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Copies page src[i] of `from` (NULL: of `cache`) to page dst[i] of `cache`,
+ * i < n, all layers; book-keeping is not touched.  Both caches have the same
+ * layers, page_size, heads_kv and head_dim.  A pair is skipped if a page is
+ * out of range, if an earlier pair has the same destination, or (within one
+ * cache) if its destination is any pair's source. */
+fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from, const int32_t* src,
+                                const int32_t* dst, int n, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Attention of one new token per sequence over the cache: query b (slot
+ * slots[b], or b if slots is NULL) attends keys j < lengths[slot] and, with
+ * window > 0, only j >= lengths[slot] - window or j < sinks (the newest token,
+ * already in the cache, is the query's own).  Query head h reads K / V head
+ * h / (heads / heads_kv).  q, o: bf16 [batch][heads][d], element strides of a
+ * batch entry and a head (multiples of 8, 16-byte aligned); lse: fp32
+ * [batch][heads].  A slot out of range, or without keys, gives O = 0 and
+ * LSE = -inf.  heads <= 65535 per batch entry in total work units, see
+ * FA_ERR_UNSUPPORTED.  workspace: fa_cache_attend_workspace_size bytes (may be
+ * 0), 256-byte aligned. */
+size_t fa_cache_attend_workspace_size(const fa_cache_t* cache, int batch, int heads, int window,
+                                      int sinks);
+fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, void* o, float* lse,
+                            int64_t q_batch, int64_t q_head, int64_t o_batch, int64_t o_head,
+                            const int32_t* slots, int batch, int heads, float softmax_scale,
+                            int window, int sinks, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* fa_status_string(fa_status_t status);
 

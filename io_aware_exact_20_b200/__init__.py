@@ -25,7 +25,7 @@ __all__ = [
     "forward_general", "backward_general", "general_workspace_size",
     "merge_partial", "accumulate_bf16", "convert_f32_bf16", "qkv_projection",
     "dropout_mask", "last_device_status", "set_wait_timeout_ns", "set_block_mask_bitmap",
-    "wait_timeout_probe", "set_nvtx", "STATUS",
+    "wait_timeout_probe", "set_nvtx", "STATUS", "PagedCache",
 ]
 
 STATUS = {
@@ -101,7 +101,22 @@ class AttentionDesc(ctypes.Structure):
     ]
 
 
+class CacheDesc(ctypes.Structure):
+    """fa_cache_t (include/fa.h), field for field."""
+    _fields_ = [
+        ("layers", ctypes.c_int), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+        ("slots", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_layer", ctypes.c_int64), ("v_layer", ctypes.c_int64),
+        ("ks", Strides), ("vs", Strides),
+        ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+    ]
+
+
 _DP = ctypes.POINTER(AttentionDesc)
+_CP = ctypes.POINTER(CacheDesc)
+_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes); must match include/fa.h
 SIGNATURES = {
@@ -130,6 +145,16 @@ SIGNATURES = {
     "fa_debug_set_block_mask_bitmap": (None, [_i]),
     "fa_debug_bounds_checking": (_i, []),
     "fa_debug_set_gqa_split": (None, [_i]),
+    "fa_cache_workspace_size": (_sz, [_CP, _i]),
+    "fa_cache_extend": (_i, [_CP, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "fa_cache_write": (_i, [_CP, _i, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i, _i, _vp]),
+    "fa_cache_fork": (_i, [_CP, _vp, _vp, _i, _vp, _sz, _vp]),
+    "fa_cache_free": (_i, [_CP, _vp, _i, _vp]),
+    "fa_cache_compact": (_i, [_CP, _vp, _vp, _sz, _vp]),
+    "fa_cache_copy_pages": (_i, [_CP, _CP, _vp, _vp, _i, _vp, _sz, _vp]),
+    "fa_cache_attend_workspace_size": (_sz, [_CP, _i, _i, _i, _i]),
+    "fa_cache_attend": (_i, [_CP, _i, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i, _i, _f, _i,
+                             _i, _vp, _sz, _vp]),
 }
 
 
@@ -581,3 +606,6 @@ def qkv_projection(x, weight, bias, batch, heads, head_dim, q=None, k=None, v=No
                                        _stream_ptr(x.device))
     _check(code, "fa_qkv_projection")
     return q, k, v
+
+
+from .paged_cache import PagedCache  # noqa: E402  (it uses the binding above)

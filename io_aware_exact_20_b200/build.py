@@ -32,7 +32,7 @@ LIB_NAME = "libfa_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_debug.cu", "fa_noalloc.cu",
-           "fa_merge.cu", "fa_proj.cu"]
+           "fa_merge.cu", "fa_proj.cu", "fa_cache.cu", "fa_decode.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]

@@ -1,0 +1,636 @@
+// Book-keeping of the paged key / value cache: growing, writing, forking,
+// freeing, compacting and copying pages.
+//
+// None of it computes: each call moves 4-byte table cells and whole K / V rows,
+// and what bounds it is the latency of a few dependent loads for the
+// book-keeping (a table cell names a page, the page's count says whether it is
+// shared) and memory bandwidth for the rows.  The number of pages that a call
+// takes or moves is known on the device only, so a call is a plan kernel, which
+// writes the list of moves, and a move kernel whose warps walk that list; the
+// host never waits and the calls can be captured.
+#include <cuda_bf16.h>
+
+#include <climits>
+
+#include "cache.h"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kPlanThreads = 1024;  // one block: its scans order entries and pages
+constexpr int kSms = 148;
+
+// Moves of a call, in the workspace: page src[i] -> dst[i], its first rows[i]
+// rows of every head and layer (0: nothing), i < *count.
+struct Moves {
+  int32_t* count;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* rows;
+};
+
+// Inclusive prefix sum over the block's threads; *total gets the sum of all.
+// Every thread of the block takes part.  smem: 33 ints.
+__device__ __forceinline__ int block_scan(int x, int* smem, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) smem[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int t = lane < static_cast<int>(blockDim.x >> 5) ? smem[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    smem[lane] = t;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? smem[warp - 1] : 0;
+  *total = smem[31];
+  __syncthreads();  // smem may be reused by the next scan
+  return x + before;
+}
+
+__device__ __forceinline__ int slot_length(const Cache& c, int s) {
+  return min(max(c.lengths[s], 0), c.max_pages * c.page_size);
+}
+
+// ---------------------------------------------------------------------------
+// extend
+// ---------------------------------------------------------------------------
+
+struct ExtendWork {
+  Moves moves;    // copies of shared last pages: entry i's at index i
+  int32_t* mark;  // [slots]: first entry that names the slot
+  int32_t* upto;  // [n]: pages needed by the entries up to and including i
+  int32_t* info;  // [n]: bit 0 its last page is shared, bit 1 it may be granted
+  int32_t* free;  // [pages]: free pages, lowest first, as many as are needed
+};
+
+__global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, const int32_t* slots,
+                                                             const int32_t* tokens, int n,
+                                                             int32_t* start, const ExtendWork w) {
+  __shared__ int scan[33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x;
+  const int P = c.page_size;
+  // the first entry of each slot
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int s = slots[i];
+    if (s >= 0 && s < c.slots) w.mark[s] = INT_MAX;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int s = slots[i];
+    if (s >= 0 && s < c.slots) atomicMin(&w.mark[s], i);
+  }
+  __syncthreads();
+  // pages each entry needs, and their running sum
+  long long need_all = 0;
+  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int need = 0, info = 0;
+    if (i < n) {
+      const int s = slots[i];
+      const int more = tokens[i];
+      if (s >= 0 && s < c.slots && w.mark[s] == i && more >= 0) {
+        const int len = slot_length(c, s);
+        const long long want = (static_cast<long long>(len) + more + P - 1) / P;
+        if (want <= c.max_pages) {
+          info = 2;
+          const int have = (len + P - 1) / P;
+          if (more > 0 && len % P != 0) {
+            const int page = c.table[static_cast<long long>(s) * c.max_pages + have - 1];
+            if (page >= 0 && page < c.pages && c.refs[page] > 1) info = 3;
+          }
+          need = static_cast<int>(want) - have + (info & 1);
+        }
+      }
+    }
+    int total = 0;
+    const int upto = block_scan(need, scan, &total);  // at most 1024 * 2^20 + 1024
+    if (i < n) {
+      const long long u = need_all + upto;
+      w.upto[i] = static_cast<int>(u < INT_MAX ? u : INT_MAX);
+      w.info[i] = info | (need > 0 ? 4 : 0);
+    }
+    need_all += total;
+  }
+  // that many free pages, or all there are
+  const int limit = static_cast<int>(need_all < c.pages ? need_all : c.pages);
+  int found = 0;
+  for (int p0 = 0; p0 < c.pages && found < limit; p0 += 4 * kPlanThreads) {
+    const int p = p0 + 4 * tid;
+    bool is_free[4];
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      is_free[u] = p + u < c.pages && c.refs[p + u] <= 0;
+      mine += is_free[u];
+    }
+    int total = 0;
+    int at = found + block_scan(mine, scan, &total) - mine;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (is_free[u]) {
+        if (at < limit) w.free[at] = p + u;
+        ++at;
+      }
+    found += total;
+  }
+  __syncthreads();
+  // grant: a warp per entry, its lanes over the entry's new table cells
+  const int lane = tid & 31;
+  for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
+    const int info = w.info[i], upto = w.upto[i];
+    const bool granted = (info & 2) && (!(info & 4) || upto <= found);
+    int copy_src = 0, copy_dst = 0, copy_rows = 0, first = -1;
+    if (granted) {
+      const int s = slots[i];
+      const int len = slot_length(c, s);
+      const int have = (len + P - 1) / P, shared = info & 1;
+      const int want = (len + tokens[i] + P - 1) / P;
+      const int need = want - have + shared;
+      int32_t* row = c.table + static_cast<long long>(s) * c.max_pages;
+      if (shared) {
+        copy_src = row[have - 1];
+        copy_dst = w.free[upto - need];
+        copy_rows = len % P;
+      }
+      __syncwarp();
+      for (int j = lane; j < need; j += 32) {
+        const int page = w.free[upto - need + j];
+        row[have - shared + j] = page;
+        c.refs[page] = 1;
+      }
+      if (lane == 0) {
+        if (shared) atomicSub(&c.refs[copy_src], 1);
+        c.lengths[s] = len + tokens[i];
+      }
+      first = len;
+    }
+    if (lane == 0) {
+      start[i] = first;
+      w.moves.src[i] = copy_src;
+      w.moves.dst[i] = copy_dst;
+      w.moves.rows[i] = copy_rows;
+    }
+  }
+  if (tid == 0) *w.moves.count = n;
+}
+
+// ---------------------------------------------------------------------------
+// moves: a warp per (move, layer, K or V, head)
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(256) move_kernel(const Cache from, const Cache to, const Moves m) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int chunks = from.d / 8;  // 16-byte pieces of a row
+  const long long per_move = 2ll * from.layers * from.heads_kv;
+  const long long items = *m.count * per_move;
+  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
+  for (long long it = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+       it < items; it += warps) {
+    const int i = static_cast<int>(it / per_move);
+    const int rows = m.rows[i];
+    if (rows == 0) continue;
+    int r = static_cast<int>(it - i * per_move);
+    const int h = r % from.heads_kv;
+    r /= from.heads_kv;
+    const int layer = r >> 1;
+    const bool is_v = (r & 1) != 0;
+    const __nv_bfloat16* src =
+        static_cast<const __nv_bfloat16*>(is_v ? from.v : from.k) +
+        (is_v ? layer * from.v_layer + m.src[i] * from.v_page + h * from.v_head
+              : layer * from.k_layer + m.src[i] * from.k_page + h * from.k_head);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) +
+                         (is_v ? layer * to.v_layer + m.dst[i] * to.v_page + h * to.v_head
+                               : layer * to.k_layer + m.dst[i] * to.k_page + h * to.k_head);
+    const long long src_row = is_v ? from.v_row : from.k_row, dst_row = is_v ? to.v_row : to.k_row;
+    for (int x = lane; x < rows * chunks; x += 32) {
+      const int row = x / chunks, col = 8 * (x - row * chunks);
+      *reinterpret_cast<uint4*>(dst + row * dst_row + col) =
+          *reinterpret_cast<const uint4*>(src + row * src_row + col);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// write: a warp per token
+// ---------------------------------------------------------------------------
+
+struct WriteParams {
+  Cache c;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long k_row, k_head, v_row, v_head;
+  const int32_t* slots;
+  const int32_t* start;
+  const int32_t* cu;
+  int layer, n, total;
+};
+
+__global__ void __launch_bounds__(256) write_kernel(const WriteParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (t >= p.total) return;
+  int i = t, within = 0;
+  if (p.cu != nullptr) {
+    // last entry that begins at or before token t (entries may be empty)
+    int lo = 0, hi = p.n;  // cu[lo] <= t < cu[hi] where t belongs to an entry
+    if (p.cu[0] > t || p.cu[p.n] <= t) return;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.cu[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    i = lo;
+    within = t - p.cu[lo];
+  }
+  const int first = p.start[i], s = p.slots[i];
+  if (first < 0 || s < 0 || s >= p.c.slots) return;
+  const long long pos = static_cast<long long>(first) + within;
+  const long long cell = pos / p.c.page_size;
+  if (cell >= p.c.max_pages) return;
+  const int page = p.c.table[static_cast<long long>(s) * p.c.max_pages + cell];
+  if (page < 0 || page >= p.c.pages) return;
+  const int row = static_cast<int>(pos - cell * p.c.page_size);
+  const int chunks = p.c.d / 8, half = p.c.heads_kv * chunks;
+  for (int x = lane; x < 2 * half; x += 32) {
+    const bool is_v = x >= half;
+    const int y = is_v ? x - half : x;
+    const int h = y / chunks, col = 8 * (y - h * chunks);
+    const __nv_bfloat16* src = is_v ? p.v + t * p.v_row + h * p.v_head + col
+                                    : p.k + t * p.k_row + h * p.k_head + col;
+    __nv_bfloat16* dst =
+        is_v ? static_cast<__nv_bfloat16*>(p.c.v) + p.layer * p.c.v_layer + page * p.c.v_page +
+                   h * p.c.v_head + row * p.c.v_row + col
+             : static_cast<__nv_bfloat16*>(p.c.k) + p.layer * p.c.k_layer + page * p.c.k_page +
+                   h * p.c.k_head + row * p.c.k_row + col;
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fork and free: a block per entry
+// ---------------------------------------------------------------------------
+
+struct ForkWork {
+  int32_t* rows;    // [n][max_pages]: the sources' table rows
+  int32_t* lens;    // [n]: their lengths, -1 for entries that are skipped
+};
+
+__global__ void __launch_bounds__(256) fork_take_kernel(const Cache c, const int32_t* src,
+                                                        const int32_t* dst, const ForkWork w) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x;
+  const int s = src[i], d = dst[i];
+  bool skip = s == d || s < 0 || s >= c.slots || d < 0 || d >= c.slots;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) skip = skip || dst[j] == d;
+  if (__syncthreads_or(skip)) {
+    if (threadIdx.x == 0) w.lens[i] = -1;
+    return;
+  }
+  const int32_t* row = c.table + static_cast<long long>(s) * c.max_pages;
+  int32_t* out = w.rows + static_cast<long long>(i) * c.max_pages;
+  for (int j = threadIdx.x; j < c.max_pages; j += blockDim.x) {
+    const int page = row[j];
+    out[j] = page;
+    if (page >= 0 && page < c.pages) atomicAdd(&c.refs[page], 1);
+  }
+  if (threadIdx.x == 0) w.lens[i] = slot_length(c, s);
+}
+
+__global__ void __launch_bounds__(256) fork_put_kernel(const Cache c, const int32_t* dst,
+                                                       const ForkWork w) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x;
+  const int len = w.lens[i];
+  if (len < 0) return;
+  const int d = dst[i];
+  int32_t* row = c.table + static_cast<long long>(d) * c.max_pages;
+  const int32_t* in = w.rows + static_cast<long long>(i) * c.max_pages;
+  for (int j = threadIdx.x; j < c.max_pages; j += blockDim.x) {
+    const int page = row[j];
+    if (page >= 0 && page < c.pages) atomicSub(&c.refs[page], 1);
+    row[j] = in[j];
+  }
+  if (threadIdx.x == 0) c.lengths[d] = len;
+}
+
+// The exchange lets a slot that is named twice go once.
+__global__ void __launch_bounds__(256) free_kernel(const Cache c, const int32_t* slots) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int s = slots[blockIdx.x];
+  if (s < 0 || s >= c.slots) return;
+  int32_t* row = c.table + static_cast<long long>(s) * c.max_pages;
+  for (int j = threadIdx.x; j < c.max_pages; j += blockDim.x) {
+    const int page = atomicExch(&row[j], -1);
+    if (page >= 0 && page < c.pages) atomicSub(&c.refs[page], 1);
+  }
+  if (threadIdx.x == 0) c.lengths[s] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------
+
+struct CompactWork {
+  Moves moves;
+  int32_t* now;  // [pages]: new number of a page that is numbered U or more
+};
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Cache c, int32_t* used,
+                                                                   const CompactWork w) {
+  __shared__ int scan[33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x;
+  int mine = 0;
+  for (int p = tid; p < c.pages; p += kPlanThreads) mine += c.refs[p] > 0;
+  int count = 0;
+  block_scan(mine, scan, &count);
+  // the k-th free page below `count` receives the k-th used one from it on
+  int holes = 0, movers = 0;
+  for (int p0 = 0; p0 < c.pages; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    const bool in_use = p < c.pages && c.refs[p] > 0;
+    const bool hole = p < count && !in_use, mover = p >= count && in_use;
+    int total = 0;
+    const int at = block_scan(hole ? 1 : mover ? 1 << 16 : 0, scan, &total);
+    if (hole) w.moves.dst[holes + (at & 0xFFFF) - 1] = p;
+    if (mover) w.moves.src[movers + (at >> 16) - 1] = p;
+    if (!mover && p >= count && p < c.pages) w.now[p] = p;
+    holes += total & 0xFFFF;
+    movers += total >> 16;
+  }
+  __syncthreads();
+  for (int k = tid; k < movers; k += kPlanThreads) {
+    const int s = w.moves.src[k], d = w.moves.dst[k];
+    w.moves.rows[k] = c.page_size;
+    w.now[s] = d;
+    c.refs[d] = c.refs[s];
+    c.refs[s] = 0;
+  }
+  if (tid == 0) {
+    *w.moves.count = movers;
+    *used = count;
+  }
+}
+
+__global__ void __launch_bounds__(256) renumber_kernel(const Cache c, const int32_t* used,
+                                                       const int32_t* now) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int count = *used;
+  const long long cells = static_cast<long long>(c.slots) * c.max_pages;
+  for (long long x = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; x < cells;
+       x += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int page = c.table[x];
+    if (page >= count && page < c.pages) c.table[x] = now[page];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// copy: which pairs are made
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(256) copy_plan_kernel(int pages_from, int pages_to, bool same,
+                                                        const int32_t* src, const int32_t* dst,
+                                                        int n, int page_size, const Moves m) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x;
+  const int s = src[i], d = dst[i];
+  bool skip = s < 0 || s >= pages_from || d < 0 || d >= pages_to;
+  for (int j = threadIdx.x; j < n; j += blockDim.x)
+    skip = skip || (j < i && dst[j] == d) || (same && src[j] == d);
+  skip = __syncthreads_or(skip);
+  if (threadIdx.x == 0) {
+    m.src[i] = s;
+    m.dst[i] = d;
+    m.rows[i] = skip ? 0 : page_size;
+    if (i == 0) *m.count = n;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// workspaces and launches
+// ---------------------------------------------------------------------------
+
+// ints, each array rounded up to 64 of them
+int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
+
+struct Carve {
+  int32_t* at;
+  int32_t* take(int64_t ints) {
+    int32_t* p = at;
+    at += round64(ints);
+    return p;
+  }
+};
+
+Moves carve_moves(Carve* w, int64_t n) {
+  Moves m;
+  m.count = w->take(1);
+  m.src = w->take(n);
+  m.dst = w->take(n);
+  m.rows = w->take(n);
+  return m;
+}
+
+// the largest of the four calls' needs
+int64_t workspace_ints(const Cache& c, int n) {
+  const int64_t extend = 64 + 5 * round64(n) + round64(c.slots) + round64(c.pages);
+  const int64_t fork = round64(static_cast<int64_t>(n) * c.max_pages) + round64(n);
+  const int64_t compact = 64 + 4 * round64(c.pages);
+  int64_t x = extend > fork ? extend : fork;
+  return x > compact ? x : compact;
+}
+
+bool workspace_ok(const Cache& c, int n, const void* ws, size_t bytes) {
+  return cache_aligned(ws, 256) && bytes >= static_cast<size_t>(workspace_ints(c, n)) * 4;
+}
+
+bool ints_ok(const void* p) { return cache_aligned(p, 4); }
+
+// Warps for every (move, layer, tensor, head) of up to `moves` moves, within
+// two waves of 8-warp blocks: the move kernel's warps walk the rest.
+unsigned move_blocks(const Cache& c, int64_t moves) {
+  const int64_t warps = moves * 2 * c.layers * c.heads_kv;
+  const int64_t blocks = (warps + 7) / 8;
+  return static_cast<unsigned>(blocks < kSms * 16 ? (blocks < 1 ? 1 : blocks) : kSms * 16);
+}
+
+fa_status_t done(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+size_t fa_cache_workspace_size(const fa_cache_t* cache, int n) {
+  fa::Cache c;
+  if (fa::cache_resolve(cache, false, &c) != FA_OK || n < 0) return 0;
+  return static_cast<size_t>(fa::workspace_ints(c, n)) * 4;
+}
+
+fa_status_t fa_cache_extend(const fa_cache_t* cache, const int32_t* slots, const int32_t* tokens,
+                            int n, int32_t* start, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  fa::Cache c;
+  const fa_status_t st = fa::cache_resolve(cache, true, &c);
+  if (st != FA_OK) return st;
+  if (n < 0) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (!fa::ints_ok(slots) || !fa::ints_ok(tokens) || !fa::ints_ok(start)) return FA_ERR_INVALID_ARG;
+  if (!fa::workspace_ok(c, n, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  fa::Carve carve{static_cast<int32_t*>(workspace)};
+  fa::ExtendWork w;
+  w.moves = fa::carve_moves(&carve, n);
+  w.upto = carve.take(n);
+  w.info = carve.take(n);
+  w.mark = carve.take(c.slots);
+  w.free = carve.take(c.pages);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fa::launch_overlapped(fa::extend_kernel, dim3(1), dim3(fa::kPlanThreads), 0, s, c,
+                                        slots, tokens, n, start, w);
+  if (e == cudaSuccess)
+    e = fa::launch_overlapped(fa::move_kernel, dim3(fa::move_blocks(c, n)), dim3(256), 0, s, c, c,
+                              w.moves);
+  return fa::done(e);
+}
+
+fa_status_t fa_cache_write(const fa_cache_t* cache, int layer, const void* k, const void* v,
+                           int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
+                           const int32_t* slots, const int32_t* start, const int32_t* cu, int n,
+                           int total, void* stream) {
+  fa::WriteParams p;
+  const fa_status_t st = fa::cache_resolve(cache, false, &p.c);
+  if (st != FA_OK) return st;
+  if (layer < 0 || layer >= p.c.layers || n < 0 || total < 0 || (cu == nullptr && total != n))
+    return FA_ERR_INVALID_ARG;
+  if (n == 0 || total == 0) return FA_OK;
+  if (!fa::cache_aligned(k, 16) || !fa::cache_aligned(v, 16) || !fa::ints_ok(slots) ||
+      !fa::ints_ok(start) || (reinterpret_cast<uintptr_t>(cu) & 3u) != 0)
+    return FA_ERR_INVALID_ARG;
+  if (!fa::cache_stride_ok(k_row, 1) || !fa::cache_stride_ok(v_row, 1) ||
+      !fa::cache_stride_ok(k_head, 1) || !fa::cache_stride_ok(v_head, 1))
+    return FA_ERR_INVALID_ARG;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_row = k_row;
+  p.k_head = k_head;
+  p.v_row = v_row;
+  p.v_head = v_head;
+  p.slots = slots;
+  p.start = start;
+  p.cu = cu;
+  p.layer = layer;
+  p.n = n;
+  p.total = total;
+  return fa::done(fa::launch_overlapped(fa::write_kernel, dim3((static_cast<unsigned>(total) + 7) / 8),
+                                        dim3(256), 0, static_cast<cudaStream_t>(stream), p));
+}
+
+fa_status_t fa_cache_fork(const fa_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  fa::Cache c;
+  const fa_status_t st = fa::cache_resolve(cache, true, &c);
+  if (st != FA_OK) return st;
+  if (n < 0) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (!fa::ints_ok(src) || !fa::ints_ok(dst)) return FA_ERR_INVALID_ARG;
+  if (!fa::workspace_ok(c, n, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  fa::Carve carve{static_cast<int32_t*>(workspace)};
+  fa::ForkWork w;
+  w.lens = carve.take(n);
+  w.rows = carve.take(static_cast<int64_t>(n) * c.max_pages);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fa::launch_overlapped(fa::fork_take_kernel, dim3(static_cast<unsigned>(n)),
+                                        dim3(256), 0, s, c, src, dst, w);
+  if (e == cudaSuccess)
+    e = fa::launch_overlapped(fa::fork_put_kernel, dim3(static_cast<unsigned>(n)), dim3(256), 0, s,
+                              c, dst, w);
+  return fa::done(e);
+}
+
+fa_status_t fa_cache_free(const fa_cache_t* cache, const int32_t* slots, int n, void* stream) {
+  fa::Cache c;
+  const fa_status_t st = fa::cache_resolve(cache, true, &c);
+  if (st != FA_OK) return st;
+  if (n < 0) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (!fa::ints_ok(slots)) return FA_ERR_INVALID_ARG;
+  return fa::done(fa::launch_overlapped(fa::free_kernel, dim3(static_cast<unsigned>(n)), dim3(256), 0,
+                                        static_cast<cudaStream_t>(stream), c, slots));
+}
+
+fa_status_t fa_cache_compact(const fa_cache_t* cache, int32_t* used, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  fa::Cache c;
+  const fa_status_t st = fa::cache_resolve(cache, true, &c);
+  if (st != FA_OK) return st;
+  if (!fa::ints_ok(used)) return FA_ERR_INVALID_ARG;
+  if (!fa::workspace_ok(c, 0, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  fa::Carve carve{static_cast<int32_t*>(workspace)};
+  fa::CompactWork w;
+  w.moves = fa::carve_moves(&carve, c.pages);
+  w.now = carve.take(c.pages);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fa::launch_overlapped(fa::compact_plan_kernel, dim3(1), dim3(fa::kPlanThreads), 0, s,
+                                        c, used, w);
+  if (e == cudaSuccess)
+    e = fa::launch_overlapped(fa::move_kernel, dim3(fa::move_blocks(c, c.pages)), dim3(256), 0, s, c, c,
+                              w.moves);
+  if (e == cudaSuccess) {
+    const int64_t blocks = (static_cast<int64_t>(c.slots) * c.max_pages + 255) / 256;
+    e = fa::launch_overlapped(fa::renumber_kernel,
+                              dim3(static_cast<unsigned>(blocks < fa::kSms * 8 ? blocks : fa::kSms * 8)),
+                              dim3(256), 0, s, c, static_cast<const int32_t*>(used),
+                              static_cast<const int32_t*>(w.now));
+  }
+  return fa::done(e);
+}
+
+fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from, const int32_t* src,
+                                const int32_t* dst, int n, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  fa::Cache to, of;
+  fa_status_t st = fa::cache_resolve(cache, false, &to);
+  if (st == FA_OK) st = fa::cache_resolve(from != nullptr ? from : cache, false, &of);
+  if (st != FA_OK) return st;
+  if (n < 0) return FA_ERR_INVALID_ARG;
+  if (of.layers != to.layers || of.page_size != to.page_size || of.heads_kv != to.heads_kv ||
+      of.d != to.d)
+    return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (!fa::ints_ok(src) || !fa::ints_ok(dst)) return FA_ERR_INVALID_ARG;
+  if (!fa::workspace_ok(to, n, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  fa::Carve carve{static_cast<int32_t*>(workspace)};
+  const fa::Moves m = fa::carve_moves(&carve, n);
+  const bool same = of.k == to.k || of.v == to.v;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fa::launch_overlapped(fa::copy_plan_kernel, dim3(static_cast<unsigned>(n)), dim3(256),
+                                        0, s, of.pages, to.pages, same, src, dst, n, to.page_size, m);
+  if (e == cudaSuccess)
+    e = fa::launch_overlapped(fa::move_kernel, dim3(fa::move_blocks(to, n)), dim3(256), 0, s, of, to, m);
+  return fa::done(e);
+}
+
+}  // extern "C"

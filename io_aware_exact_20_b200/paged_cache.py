@@ -1,0 +1,187 @@
+"""Paged key / value cache: the tensors of ``fa_cache_t`` (include/fa.h) and its
+calls.  Everything the calls decide (which pages are free, which are shared,
+what has to be copied) is decided on the device, so none of them waits for it
+and all of them can be captured in a CUDA graph."""
+
+from __future__ import annotations
+
+import ctypes
+
+import io_aware_exact_20_b200 as _fa
+
+
+class PagedCache:
+    """Keys and values of up to ``slots`` sequences in pages of a common pool.
+
+    k, v      bf16 [layers, pages, heads_kv, page_size, d], any strides with d
+              contiguous (multiples of 8 elements)
+    table     int32 [slots, max_pages]: page numbers, -1 where there is none
+    lengths   int32 [slots]: tokens of each sequence
+    refs      int32 [pages]: slots that hold a page, 0: free
+
+    The tensors stay the caller's (they may be views of one buffer) and are
+    changed in place; ``allocate`` makes an empty cache.  Slots are given as int32 device
+    tensors.  Calls on one cache have to be ordered: one stream, or events."""
+
+    def __init__(self, k, v, table, lengths, refs):
+        import torch
+        if k.dim() != 5 or v.shape != k.shape:
+            raise ValueError("k, v: [layers, pages, heads_kv, page_size, d] tensors of one shape")
+        if table.dim() != 2 or lengths.shape != table.shape[:1] or refs.shape != k.shape[1:2]:
+            raise ValueError("table [slots, max_pages], lengths [slots], refs [pages] are expected")
+        for name, t in (("k", k), ("v", v)):
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.device != k.device:
+                raise ValueError(f"{name}: bfloat16 on one CUDA device is expected")
+            if t.stride(4) != 1:
+                raise ValueError(f"{name}: the head dimension must be contiguous")
+        for name, t in (("table", table), ("lengths", lengths), ("refs", refs)):
+            if t.device != k.device or t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError(f"{name}: contiguous int32 on the device of k is expected")
+        self.k, self.v, self.table, self.lengths, self.refs = k, v, table, lengths, refs
+        self.layers, self.pages, self.heads_kv, self.page_size, self.head_dim = k.shape
+        self.slots, self.max_pages = table.shape
+        self.device = k.device
+        a = _fa.CacheDesc()
+        a.layers, a.pages, a.page_size = self.layers, self.pages, self.page_size
+        a.heads_kv, a.head_dim = self.heads_kv, self.head_dim
+        a.slots, a.max_pages = self.slots, self.max_pages
+        a.k, a.v = k.data_ptr(), v.data_ptr()
+        a.k_layer, a.v_layer = k.stride(0), v.stride(0)
+        a.ks = _fa.Strides(k.stride(1), k.stride(2), k.stride(3))
+        a.vs = _fa.Strides(v.stride(1), v.stride(2), v.stride(3))
+        a.table, a.lengths, a.refs = table.data_ptr(), lengths.data_ptr(), refs.data_ptr()
+        self._desc, self._ref = a, ctypes.byref(a)
+        self._lib = _fa.library()
+        if self._lib.fa_cache_workspace_size(self._ref, 0) == 0:
+            raise ValueError("the cache's sizes, strides or alignment are not supported (fa.h)")
+
+    @classmethod
+    def allocate(cls, layers, pages, page_size, heads_kv, head_dim, slots, max_pages, device="cuda"):
+        """An empty cache: every page free, every slot empty."""
+        import torch
+        shape = (layers, pages, heads_kv, page_size, head_dim)
+        kv = [torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)]
+        ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(*kv, ints(slots, max_pages).fill_(-1), ints(slots), ints(pages))
+
+    def _ints(self, name, t, n=None):
+        import torch
+        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous 1-D int32 tensor on the cache's device is expected")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: {n} entries are expected, got {t.shape[0]}")
+        return t.data_ptr()
+
+    def _workspace(self, n):
+        import torch
+        size = self._lib.fa_cache_workspace_size(self._ref, n)
+        return torch.empty(size, dtype=torch.uint8, device=self.device), size
+
+    def _call(self, name, *args):
+        """The C call on the cache's device and that device's current stream."""
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            code = getattr(self._lib, name)(self._ref, *args, _fa._stream_ptr(self.device))
+        else:
+            with torch.cuda.device(self.device):
+                code = getattr(self._lib, name)(self._ref, *args, _fa._stream_ptr(self.device))
+        _fa._check(code, name)
+
+    @_fa._nvtx("fa.cache.extend")
+    def extend(self, slots, tokens):
+        """Grows slots[i] by tokens[i]; returns start (int32 [n]), each entry's
+        first new position, -1 where it was not granted (fa_cache_extend)."""
+        import torch
+        n = slots.shape[0]
+        start = torch.empty(n, dtype=torch.int32, device=self.device)
+        ws, size = self._workspace(n)
+        self._call("fa_cache_extend", self._ints("slots", slots), self._ints("tokens", tokens, n), n,
+                   start.data_ptr(), ws.data_ptr(), size)
+        return start
+
+    @_fa._nvtx("fa.cache.write")
+    def write(self, layer, k, v, slots, start, cu_seqlens=None):
+        """Writes k, v (bf16 [T, heads_kv, d]) of one layer to the positions
+        start[i], start[i] + 1, ... of slots[i]: one row per entry, or with
+        cu_seqlens (int32 [n + 1]) rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1."""
+        import torch
+        n = slots.shape[0]
+        for name, t in (("k", k), ("v", v)):
+            if t.dim() != 3 or t.shape[1:] != (self.heads_kv, self.head_dim) or t.shape != k.shape:
+                raise ValueError(f"{name}: [T, {self.heads_kv}, {self.head_dim}] is expected")
+            if t.dtype != torch.bfloat16 or t.device != self.device or t.stride(2) != 1:
+                raise ValueError(f"{name}: bfloat16 on the cache's device, d contiguous, is expected")
+        cu = None if cu_seqlens is None else self._ints("cu_seqlens", cu_seqlens, n + 1)
+        if cu is None and k.shape[0] != n:
+            raise ValueError("write: one row per slot is expected without cu_seqlens")
+        self._call("fa_cache_write", layer, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                   v.stride(0), v.stride(1), self._ints("slots", slots),
+                   self._ints("start", start, n), cu, n, k.shape[0])
+
+    @_fa._nvtx("fa.cache.attend")
+    def attend(self, layer, q, slots=None, scale=None, window=0, sinks=0, out=None, lse=None):
+        """O, LSE of one query per sequence (q bf16 [B, H, d]) over the keys of
+        its slot (slots int32 [B]; None: slot b for query b), with a window and
+        first tokens as in forward_general.  The newest token has to be in the
+        cache.  LSE: fp32 [B, H]."""
+        import torch
+        if q.dim() != 3 or q.shape[2] != self.head_dim:
+            raise ValueError(f"q: [B, H, {self.head_dim}] is expected")
+        B, H, d = q.shape
+        if H < 1 or H % self.heads_kv:
+            raise ValueError("q's heads must be a multiple of the cache's")
+        if out is None:
+            out = torch.empty((B, H, d), dtype=torch.bfloat16, device=self.device)
+        if lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=self.device)
+        elif (lse.shape != (B, H) or lse.dtype != torch.float32 or lse.device != self.device
+              or not lse.is_contiguous()):
+            raise ValueError(f"lse: contiguous float32 {(B, H)} on the cache's device is expected")
+        for name, t in (("q", q), ("out", out)):
+            if (t.dtype != torch.bfloat16 or t.device != self.device or t.shape != q.shape
+                    or t.stride(2) != 1):
+                raise ValueError(f"{name}: bfloat16 {tuple(q.shape)} on the cache's device, d "
+                                 "contiguous, is expected")
+        window, sinks = _fa._window(window, sinks)
+        size = self._lib.fa_cache_attend_workspace_size(self._ref, B, H, window, sinks)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+        self._call("fa_cache_attend", layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                   q.stride(0), q.stride(1), out.stride(0), out.stride(1),
+                   None if slots is None else self._ints("slots", slots, B), B, H,
+                   d ** -0.5 if scale is None else float(scale), window, sinks,
+                   None if ws is None else ws.data_ptr(), size)
+        return out, lse
+
+    @_fa._nvtx("fa.cache.fork")
+    def fork(self, src, dst):
+        """Slot dst[i] lets its pages go and shares src[i]'s (fa_cache_fork)."""
+        n = src.shape[0]
+        ws, size = self._workspace(n)
+        self._call("fa_cache_fork", self._ints("src", src), self._ints("dst", dst, n), n,
+                   ws.data_ptr(), size)
+
+    @_fa._nvtx("fa.cache.free")
+    def free(self, slots):
+        """The slots let their pages go and become empty."""
+        self._call("fa_cache_free", self._ints("slots", slots), slots.shape[0])
+
+    @_fa._nvtx("fa.cache.compact")
+    def compact(self):
+        """Moves the pages in use into the lowest numbers; returns how many there
+        are (int32 [1], on the device)."""
+        import torch
+        used = torch.empty(1, dtype=torch.int32, device=self.device)
+        ws, size = self._workspace(0)
+        self._call("fa_cache_compact", used.data_ptr(), ws.data_ptr(), size)
+        return used
+
+    @_fa._nvtx("fa.cache.copy_pages")
+    def copy_pages(self, src, dst, source=None):
+        """Copies page src[i] (of the cache `source`, default this one) to page
+        dst[i], every layer; the book-keeping stays (fa_cache_copy_pages)."""
+        if source is not None and source.device != self.device:
+            raise ValueError("copy_pages: both caches on one device are expected")
+        n = src.shape[0]
+        ws, size = self._workspace(n)
+        self._call("fa_cache_copy_pages", None if source is None else source._ref,
+                   self._ints("src", src), self._ints("dst", dst, n), n, ws.data_ptr(), size)
