@@ -923,6 +923,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // padding keys need masking; the choice must be warp-uniform (the TMEM
       // loads and stores in both versions are warp-collective)
       const bool masked = __any_sync(0xffffffffu, diag || !key_live || (WIN && qmax < 128));
+      // window: the queries that see this thread's key, as bits, per half of
+      // the warpgroup's 64
+      uint32_t seen[2] = {0u, 0u};
+      if constexpr (WIN) {
+        if (key_live) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int q0 = 64 * wg + 32 * c;
+            seen[c] = low_bits(qmax - q0) & ~low_bits(w.causal ? qmin - q0 : 0);
+          }
+        }
+      }
 
       // P for queries qoff + 4 k4 + [0, 4) of this key: exp2(S^T scale log2e - LSE log2e)
       auto p_quad = [&](auto mask_tag, const uint32_t* sv, int qoff, int k4, float pv[4]) {
@@ -939,8 +951,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if constexpr (MASKED) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!key_live || (diag && qoff + 4 * k4 + e < qmin) ||
-                (WIN && qoff + 4 * k4 + e >= qmax))
+            if constexpr (WIN)
+              pv[e] = (seen[(qoff >> 5) & 1] >> (4 * k4 + e)) & 1u ? pv[e] : 0.f;
+            else if (!key_live || (diag && qoff + 4 * k4 + e < qmin))
               pv[e] = 0.f;
         }
       };

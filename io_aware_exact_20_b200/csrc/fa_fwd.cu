@@ -610,10 +610,17 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::MIN_BLOCKS)
         if (need_mask) {
           const int lim = w.causal ? min(w.kv_len - j0, i + w.off - j0 + 1) : (w.kv_len - j0);
           if constexpr (WIN) {
+            // visible keys as bits: tested one by one, the two bounds compile to
+            // a branch per key (6.7 us for a masked tile at d = 128)
             const int lo = i + w.off - w.win + 1 - j0, first = w.sinks - j0;
 #pragma unroll
-            for (int j = 0; j < KW; ++j)
-              if (j >= lim || (j < lo && j >= first)) sr[j] = __float_as_uint(-INFINITY);
+            for (int j32 = 0; j32 < KW; j32 += 32) {
+              const uint32_t seen =
+                  low_bits(lim - j32) & (~low_bits(lo - j32) | low_bits(first - j32));
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                sr[j32 + j] = (seen >> j) & 1u ? sr[j32 + j] : __float_as_uint(-INFINITY);
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < KW; ++j)

@@ -97,6 +97,11 @@ __device__ __forceinline__ bool in_bounds(int* status, long long off, long long 
 #define FA_IN_BOUNDS(status, off, width, extent) true
 #endif
 
+// Bits 0 .. n-1 of a word (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
+}
+
 // Element strides of a [batch, head, row, d] view (d is contiguous).
 struct Strides {
   long long b, h, r;
