@@ -11,6 +11,16 @@
 // every warp works on its own tiles of KT keys with its own ring of
 // asynchronous copies, so that no warp waits for another before the end.
 //
+// The work is cut evenly whatever the lengths are: each (sequence, K / V head,
+// block of heads) is a row of block tiles (kWarps warp tiles), the rows of the
+// batch lie end to end, and block c of the grid takes the c-th of equal shares,
+// found from the lengths on the device.  A row that ends in another share than
+// it begins is written as one partial result per share (fp32 sums with their
+// maximum and row sum) and joined, in the order of the shares, by a second
+// kernel; other rows are written at once.  One block per row instead took
+// 1600 us for two sequences of 131072 keys (four K / V heads, d = 128), where
+// eight blocks had work, and 117 us for 64 ragged ones that the longest held up.
+//
 // Visible keys are counted u = 0 .. n_vis - 1: the first `sinks` that the window
 // does not reach, then the window.  A tile is KT consecutive u, each with its
 // own table lookup, so pages may be of any size, tiles may straddle pages, and
@@ -43,6 +53,11 @@ struct AttendParams {
   int head_blocks;   // blocks of up to 16 query heads per K / V head
   float scale_log2;  // softmax_scale * log2(e)
   int window, sinks;
+  // partial results of the shares, null where no row can be cut
+  long long* tiles_upto;  // [batch + 1]: block tiles of one K / V head's rows before each sequence,
+                          // then the number of shares
+  float2* part_stat;      // [2 * grid][16]: maximum (log2 units), row sum
+  float* part_acc;        // [2 * grid][16][D]
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -88,7 +103,18 @@ struct DecodeCfg {
   static constexpr uint32_t OFF_VALID = kWarps * WARP;  // [warp][stage] key bits
   static constexpr uint32_t SMEM = OFF_VALID + kWarps * STAGES * 4;
   static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
+  static constexpr int BT = kWarps * KT;         // keys of a block tile
 };
+
+constexpr int kThreads = kWarps * 32;
+// A share is at least this many block tiles (of the whole batch's): smaller
+// ones cost more in joining than they save.
+constexpr int kMinShare = 2;
+
+// The share that holds block tile f: shares are [c W / n, (c + 1) W / n).
+__device__ __forceinline__ int share_of(long long f, long long W, int n) {
+  return static_cast<int>(((f + 1) * n - 1) / W);
+}
 
 // Keys a query sees: u -> key position (see the head of the file).
 struct Visible {
@@ -104,31 +130,33 @@ __device__ __forceinline__ Visible visible_of(int n, int window, int sinks) {
   return s;
 }
 
+// Eight columns of query head h of sequence b: O = out / sum, LSE = ln2 (m + log2 sum).
+__device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, int col, float m, float sum,
+                                          const float (&out)[8]) {
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) =
+      make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
+                 pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
+  if (col == 0)
+    p.lse[static_cast<long long>(b) * p.heads + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// Block tiles [t0, t1) of one row: sequence b in `slot` with n keys, K / V head
+// hk, block hb of its query heads.  The whole row (t0 = 0, t1 = row_tiles) is
+// written to O and LSE, a part of it to the share's partial results: index 1
+// where the row begins in this share, 0 where it goes on.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, DecodeCfg<D>::MIN_BLOCKS)
-    attend_kernel(const AttendParams p) {
+__device__ __forceinline__ void attend_segment(const AttendParams& p, uint8_t* smem, uint32_t ring,
+                                               uint32_t* valid, int b, int slot, int n, int hk, int hb,
+                                               int t0, int t1, int row_tiles, int share) {
   using C = DecodeCfg<D>;
   constexpr int KT = C::KT, STAGES = C::STAGES;
-  griddep_wait();
-  griddep_launch_dependents();
-  extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q4 = lane & 3;  // row and column group of the matrix fragments
-
-  // this block's sequence, K / V head and block of query heads
-  int unit = blockIdx.x;
-  const int hb = unit % p.head_blocks;
-  unit /= p.head_blocks;
-  const int hk = unit % p.c.heads_kv;
-  const int b = unit / p.c.heads_kv;
   const int h0 = hk * p.group + hb * 16;               // first query head
   const int hn = min(16, p.group - hb * 16);           // query heads
-  const int slot = p.slots != nullptr ? p.slots[b] : b;
-  int n = 0;
-  if (slot >= 0 && slot < p.c.slots)
-    n = min(max(p.c.lengths[slot], 0), p.c.max_pages * p.c.page_size);
   const Visible vis = visible_of(n, p.window, p.sinks);
-  const int tiles = (vis.count + KT - 1) / KT;
+  const int tiles = min(t1 * kWarps, (vis.count + KT - 1) / KT);  // end, in warp tiles
   const int32_t* pages = p.c.table + static_cast<long long>(slot) * p.c.max_pages;
 
   // Q as the A operand: rows g and g + 8, zero past the block's heads and past d
@@ -145,9 +173,6 @@ __global__ void __launch_bounds__(kWarps * 32, DecodeCfg<D>::MIN_BLOCKS)
                         : 0u;
       }
   }
-
-  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
-  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
 
   // K and V element offsets of this lane's key of a tile (lane & (KT - 1)), -1: none
   struct Row {
@@ -197,17 +222,22 @@ __global__ void __launch_bounds__(kWarps * 32, DecodeCfg<D>::MIN_BLOCKS)
     for (int u = 0; u < 4; ++u) o[i][u] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8; l: this lane's part
 
-  // tiles warp, warp + kWarps, ...
-  int fill = warp;
+  // tiles t0 kWarps + warp, + kWarps, ...
+  int fill = t0 * kWarps + warp;
+  {
+    Row ahead[STAGES - 1];
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) {
-    if (fill < tiles) load(s, locate(fill));
-    cp_async_commit();
-    fill += kWarps;
+    for (int s = 0; s < STAGES - 1; ++s) ahead[s] = locate(fill + s * kWarps);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      if (fill < tiles) load(s, ahead[s]);
+      cp_async_commit();
+      fill += kWarps;
+    }
   }
   Row next = locate(fill);
   int stage = 0;
-  for (int tile = warp; tile < tiles; tile += kWarps) {
+  for (int tile = t0 * kWarps + warp; tile < tiles; tile += kWarps) {
     // the next free stage was read in the previous round
     __syncwarp();
     {
@@ -319,7 +349,9 @@ __global__ void __launch_bounds__(kWarps * 32, DecodeCfg<D>::MIN_BLOCKS)
     *reinterpret_cast<float2*>(a + 8 * D) = make_float2(o[i][2], o[i][3]);
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < hn * (D / 8); x += kWarps * 32) {
+  const bool whole = t0 == 0 && t1 == row_tiles;
+  const long long part = 2ll * share + (t0 == 0 ? 1 : 0);
+  for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
     const int r = x / (D / 8), col = 8 * (x % (D / 8));
     if (col >= p.c.d) continue;
     float mm = -INFINITY;
@@ -334,21 +366,230 @@ __global__ void __launch_bounds__(kWarps * 32, DecodeCfg<D>::MIN_BLOCKS)
       const float2 st = stat[w * 16 + r];
       const float f = fast_exp2(st.x - ref);
       sum += f * st.y;
+      const float4* a = reinterpret_cast<const float4*>(acc + (w * 16 + r) * D + col);
+      const float4 a0 = a[0], a1 = a[1];
+      const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = fmaf(f, acc[(w * 16 + r) * D + col + e], out[e]);
+      for (int e = 0; e < 8; ++e) out[e] = fmaf(f, v[e], out[e]);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    *reinterpret_cast<uint4*>(p.o + b * p.o_batch + (h0 + r) * p.o_head + col) =
-        make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
-                   pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
-    if (col == 0)
-      p.lse[static_cast<long long>(b) * p.heads + h0 + r] =
-          sum > 0.f ? (mm + log2f(sum)) * kLn2 : -INFINITY;
+    if (whole) {
+      write_row(p, b, h0 + r, col, mm, sum, out);
+    } else {
+      float4* a = reinterpret_cast<float4*>(p.part_acc + (part * 16 + r) * D + col);
+      a[0] = make_float4(out[0], out[1], out[2], out[3]);
+      a[1] = make_float4(out[4], out[5], out[6], out[7]);
+      if (col == 0) p.part_stat[part * 16 + r] = make_float2(mm, sum);
+    }
   }
+  __syncthreads();  // the next segment fills the ring again
 }
 
 template <int D>
-cudaError_t launch_attend(const AttendParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_kernel(const AttendParams p) {
+  using C = DecodeCfg<D>;
+  constexpr int STAGES = C::STAGES;
+  griddep_wait();
+  griddep_launch_dependents();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- the shares: block tiles of every sequence, their sum and this block's part
+  __shared__ int s_len[kThreads], s_tiles[kThreads], s_slot[kThreads];
+  __shared__ long long s_upto[kThreads];
+  __shared__ long long s_scan[kWarps];
+  const int rows_per_seq = p.c.heads_kv * p.head_blocks;
+  auto load_seq = [&](int b) {  // length and block tiles of sequence b, this thread's
+    int n = 0, slot = -1;
+    if (b < p.batch) {
+      slot = p.slots != nullptr ? p.slots[b] : b;
+      if (slot >= 0 && slot < p.c.slots)
+        n = min(max(p.c.lengths[slot], 0), p.c.max_pages * p.c.page_size);
+    }
+    s_len[threadIdx.x] = n;
+    s_slot[threadIdx.x] = slot;
+    s_tiles[threadIdx.x] = (visible_of(n, p.window, p.sinks).count + C::BT - 1) / C::BT;
+    return static_cast<long long>(s_tiles[threadIdx.x]);
+  };
+  // inclusive prefix sum over the block; *total: the sum of all
+  auto scan = [&](long long x, long long* total) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      all += s_scan[w];
+    }
+    *total = all;
+    return x + before;
+  };
+  long long sum = 0;  // block tiles of one row per sequence
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    long long part = 0;
+    scan(load_seq(b0 + threadIdx.x), &part);
+    sum += part;
+  }
+  const long long W = sum * rows_per_seq;
+  const long long want = (W + kMinShare - 1) / kMinShare;
+  const int shares = want < 1 ? 1 : want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
+  const bool keeper = blockIdx.x == 0 && p.tiles_upto != nullptr;  // leaves the plan to the joining kernel
+  if (keeper && threadIdx.x == 0) p.tiles_upto[p.batch + 1] = shares;
+  const int share = blockIdx.x;
+  const long long lo = share < shares ? share * W / shares : W;
+  const long long hi = share < shares ? (share + 1) * W / shares : W;
+
+  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
+  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
+
+  long long chunk_lo = 0;  // block tile at which this chunk of sequences begins
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    long long part = 0;
+    const long long mine = load_seq(b0 + threadIdx.x);
+    const long long upto = scan(mine, &part);
+    s_upto[threadIdx.x] = upto;
+    if (keeper && b0 + static_cast<int>(threadIdx.x) < p.batch) {
+      p.tiles_upto[b0 + threadIdx.x + 1] = chunk_lo / rows_per_seq + upto;
+      if (b0 + threadIdx.x == 0) p.tiles_upto[0] = 0;
+    }
+    // rows without keys belong to no share: block 0 writes them
+    __syncthreads();
+    if (blockIdx.x == 0) {
+      for (int j = 0; j < min(kThreads, p.batch - b0); ++j) {
+        if (s_tiles[j] != 0) continue;
+        const int b = b0 + j;
+        for (int x = threadIdx.x; x < p.heads * (p.c.d / 8); x += kThreads) {
+          const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
+          *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
+          if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
+        }
+      }
+    }
+    const long long chunk_hi = chunk_lo + part * rows_per_seq;
+    const long long from = lo > chunk_lo ? lo : chunk_lo, end = hi < chunk_hi ? hi : chunk_hi;
+    for (long long f = from; f < end;) {
+      // the sequence of block tile f: the first whose running sum passes it
+      const long long fs = (f - chunk_lo) / rows_per_seq;
+      int bl = 0;
+      {
+        int a = 0, z = kThreads - 1;
+        while (a < z) {
+          const int mid = (a + z) / 2;
+          if (s_upto[mid] > fs) z = mid;
+          else a = mid + 1;
+        }
+        bl = a;
+      }
+      const int row_tiles = s_tiles[bl];
+      const long long seq_lo = chunk_lo + (s_upto[bl] - row_tiles) * rows_per_seq;
+      const int rs = static_cast<int>((f - seq_lo) / row_tiles);  // (K / V head, block of heads)
+      const long long row_lo = seq_lo + static_cast<long long>(rs) * row_tiles;
+      const int t0 = static_cast<int>(f - row_lo);
+      const int t1 = static_cast<int>((end - row_lo < row_tiles ? end - row_lo : row_tiles));
+      f = row_lo + t1;
+      attend_segment<D>(p, smem, ring, valid, b0 + bl, s_slot[bl], s_len[bl], rs / p.head_blocks,
+                        rs % p.head_blocks, t0, t1, row_tiles, share);
+    }
+    chunk_lo = chunk_hi;
+    __syncthreads();  // the next chunk overwrites the sequences
+  }
+}
+
+// Joins the parts of rows that were cut: a block per (sequence, query head),
+// D / 8 threads over the columns, kJoinThreads / (D / 8) groups over the parts.
+constexpr int kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
+  constexpr int TPR = D / 8, GROUPS = kJoinThreads / TPR;
+  __shared__ float2 stat[GROUPS];
+  __shared__ float acc[GROUPS][D];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
+  const long long before = p.tiles_upto[b], row_tiles = p.tiles_upto[b + 1] - before;
+  const int rows_per_seq = p.c.heads_kv * p.head_blocks;
+  const long long W = p.tiles_upto[p.batch] * rows_per_seq;
+  const int shares = static_cast<int>(p.tiles_upto[p.batch + 1]);
+  if (row_tiles == 0) return;
+  const int hk = h / p.group, hb = (h - hk * p.group) / 16, r = (h - hk * p.group) % 16;
+  const long long row_lo = before * rows_per_seq + (hk * p.head_blocks + hb) * row_tiles;
+  const int c0 = share_of(row_lo, W, shares), c1 = share_of(row_lo + row_tiles - 1, W, shares);
+  if (c0 == c1) return;  // written already
+  const int group = threadIdx.x / TPR, col = 8 * (threadIdx.x % TPR);
+  float m = -INFINITY, sum = 0.f, out[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = 0.f;
+#pragma unroll 4
+  for (int c = c0 + group; c <= c1; c += GROUPS) {
+    const long long part = (2ll * c + (c == c0 ? 1 : 0)) * 16 + r;
+    const float2 st = p.part_stat[part];
+    const float4* a = reinterpret_cast<const float4*>(p.part_acc + part * D + col);
+    const float4 a0 = a[0], a1 = a[1];
+    const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    const float mm = fmaxf(m, st.x), ref = mm == -INFINITY ? 0.f : mm;
+    const float fo = fast_exp2(m - ref), fn = fast_exp2(st.x - ref);
+    m = mm;
+    sum = sum * fo + st.y * fn;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = out[e] * fo + v[e] * fn;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[group][col + e] = out[e];
+  if (col == 0) stat[group] = make_float2(m, sum);
+  __syncthreads();
+  if (group != 0 || col >= p.c.d) return;
+  float mm = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < GROUPS; ++w) mm = fmaxf(mm, stat[w].x);
+  const float ref = mm == -INFINITY ? 0.f : mm;
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < GROUPS; ++w) {
+    const float f = fast_exp2(stat[w].x - ref);
+    sum += f * stat[w].y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = fmaf(f, acc[w][col + e], out[e]);
+  }
+  write_row(p, b, h, col, mm, sum, out);
+}
+
+// Grid and workspace of a call, from what the host knows: the longest that a
+// sequence may see.  One block per resident slot of the GPU, fewer where the
+// batch cannot have that many block tiles; no row can be cut, and none has to
+// be joined, where none can have more than one.
+struct Plan {
+  long long grid;
+  bool cut;
+  size_t off_stat, off_acc, bytes;
+};
+
+Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
+  const int D = c.d <= 64 ? 64 : c.d <= 128 ? 128 : 256;
+  const int BT = D == 64 ? DecodeCfg<64>::BT : D == 128 ? DecodeCfg<128>::BT : DecodeCfg<256>::BT;
+  const int per_sm = D == 256 ? DecodeCfg<256>::MIN_BLOCKS : DecodeCfg<128>::MIN_BLOCKS;
+  long long most = static_cast<long long>(c.max_pages) * c.page_size;
+  if (window > 0 && static_cast<long long>(window) + sinks < most) most = static_cast<long long>(window) + sinks;
+  const long long tiles = (most + BT - 1) / BT;
+  const long long rows = static_cast<long long>(batch) * c.heads_kv * ((heads / c.heads_kv + 15) / 16);
+  Plan p;
+  p.grid = rows * tiles < 148ll * per_sm ? rows * tiles : 148ll * per_sm;
+  p.cut = tiles > 1;
+  p.off_stat = ((static_cast<size_t>(batch) + 2) * 8 + 255) / 256 * 256;
+  p.off_acc = p.off_stat + static_cast<size_t>(p.grid) * 2 * 16 * sizeof(float2);
+  p.bytes = p.cut ? p.off_acc + static_cast<size_t>(p.grid) * 2 * 16 * D * sizeof(float) : 0;
+  return p;
+}
+
+template <int D>
+cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t stream) {
   using C = DecodeCfg<D>;
   static_assert(kWarps * 16 * (8 + D * 4) <= C::OFF_VALID, "the warps' parts fit the ring");
   auto kern = attend_kernel<D>;
@@ -358,16 +599,20 @@ cudaError_t launch_attend(const AttendParams& p, cudaStream_t stream) {
                                 static_cast<int>(C::SMEM));
   });
   if (e != cudaSuccess) return e;
-  const long long units = static_cast<long long>(p.batch) * p.c.heads_kv * p.head_blocks;
-  return launch_overlapped(kern, dim3(static_cast<unsigned>(units)), dim3(kWarps * 32), C::SMEM,
-                           stream, p);
-}
-
-// Work units of a call: 0 if there are too many for a grid.
-long long units_of(const Cache& c, int batch, int heads) {
-  const int blocks = (heads / c.heads_kv + 15) / 16;
-  const long long units = static_cast<long long>(batch) * c.heads_kv * blocks;
-  return units <= 0x7FFFFFFF ? units : 0;
+  const Plan plan = plan_of(p.c, p.batch, p.heads, p.window, p.sinks);
+  AttendParams a = p;
+  if (plan.cut) {
+    char* ws = static_cast<char*>(workspace);
+    a.tiles_upto = reinterpret_cast<long long*>(ws);
+    a.part_stat = reinterpret_cast<float2*>(ws + plan.off_stat);
+    a.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
+  }
+  cudaError_t r = launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), dim3(kThreads), C::SMEM,
+                                    stream, a);
+  if (r == cudaSuccess && plan.cut)
+    r = launch_overlapped(join_kernel<D>, dim3(static_cast<unsigned>(p.batch * p.heads)),
+                          dim3(kJoinThreads), 0, stream, a);
+  return r;
 }
 
 }  // namespace
@@ -377,8 +622,11 @@ extern "C" {
 
 size_t fa_cache_attend_workspace_size(const fa_cache_t* cache, int batch, int heads, int window,
                                       int sinks) {
-  (void)cache, (void)batch, (void)heads, (void)window, (void)sinks;
-  return 0;
+  fa::Cache c;
+  if (fa::cache_resolve(cache, false, &c) != FA_OK || batch < 1 || heads < 1 || heads % c.heads_kv ||
+      window < 0 || sinks < 0)
+    return 0;
+  return fa::plan_of(c, batch, heads, window, sinks).bytes;
 }
 
 fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, void* o, float* lse,
@@ -400,7 +648,9 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   if (batch == 0) return FA_OK;
   if (!fa::cache_aligned(q, 16) || !fa::cache_aligned(o, 16) || !fa::cache_aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
-  if (fa::units_of(p.c, batch, heads) == 0) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * heads > 0x7FFFFFFF) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa::plan_of(p.c, batch, heads, window, sinks).bytes;
+  if (need > 0 && (!fa::cache_aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_WORKSPACE;
   p.k = static_cast<const __nv_bfloat16*>(p.c.k) + layer * p.c.k_layer;
   p.v = static_cast<const __nv_bfloat16*>(p.c.v) + layer * p.c.v_layer;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -418,11 +668,13 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * fa::kLog2e);
   p.window = window;
   p.sinks = sinks;
-  (void)workspace, (void)workspace_bytes;
+  p.tiles_upto = nullptr;
+  p.part_stat = nullptr;
+  p.part_acc = nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p.c.d <= 64    ? fa::launch_attend<64>(p, s)
-                        : p.c.d <= 128 ? fa::launch_attend<128>(p, s)
-                                       : fa::launch_attend<256>(p, s);
+  const cudaError_t e = p.c.d <= 64    ? fa::launch_attend<64>(p, workspace, s)
+                        : p.c.d <= 128 ? fa::launch_attend<128>(p, workspace, s)
+                                       : fa::launch_attend<256>(p, workspace, s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
