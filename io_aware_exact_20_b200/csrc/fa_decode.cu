@@ -12,14 +12,12 @@
 // asynchronous copies, so that no warp waits for another before the end.
 //
 // The work is cut evenly whatever the lengths are: each (sequence, K / V head,
-// block of heads) is a row of block tiles (kWarps warp tiles), the rows of the
-// batch lie end to end, and block c of the grid takes the c-th of equal shares,
-// found from the lengths on the device.  A row that ends in another share than
-// it begins is written as one partial result per share (fp32 sums with their
-// maximum and row sum) and joined, in the order of the shares, by a second
-// kernel; other rows are written at once.  One block per row instead took
-// 1600 us for two sequences of 131072 keys (four K / V heads, d = 128), where
-// eight blocks had work, and 117 us for 64 ragged ones that the longest held up.
+// block of heads) is a row of tiles, the rows of the batch lie end to end, and
+// every warp of the grid takes an equal share of them, found from the lengths
+// on the device.  Its copies run ahead across the ends of rows.  A row that ends
+// in another share than it begins is written as one partial result per share
+// (fp32 sums with their maximum and row sum) and joined, in the order of the
+// shares, by a second kernel; other rows are written at once.
 //
 // Visible keys are counted u = 0 .. n_vis - 1: the first `sinks` that the window
 // does not reach, then the window.  A tile is KT consecutive u, each with its
@@ -54,10 +52,10 @@ struct AttendParams {
   float scale_log2;  // softmax_scale * log2(e)
   int window, sinks;
   // partial results of the shares, null where no row can be cut
-  long long* tiles_upto;  // [batch + 1]: block tiles of one K / V head's rows before each sequence,
-                          // then the number of shares
-  float2* part_stat;      // [2 * grid][16]: maximum (log2 units), row sum
-  float* part_acc;        // [2 * grid][16][D]
+  long long* tiles_upto;  // [batch + 1]: tiles of one row of every sequence before each, then
+                          // the number of shares
+  float2* part_stat;      // [2 * shares][16]: maximum (log2 units), row sum
+  float* part_acc;        // [2 * shares][16][D]
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -103,15 +101,14 @@ struct DecodeCfg {
   static constexpr uint32_t OFF_VALID = kWarps * WARP;  // [warp][stage] key bits
   static constexpr uint32_t SMEM = OFF_VALID + kWarps * STAGES * 4;
   static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
-  static constexpr int BT = kWarps * KT;         // keys of a block tile
 };
 
 constexpr int kThreads = kWarps * 32;
-// A share is at least this many block tiles (of the whole batch's): smaller
-// ones cost more in joining than they save.
-constexpr int kMinShare = 2;
+// A share is at least this many tiles (of the whole batch's): smaller ones
+// cost more in joining than they save.
+constexpr int kMinShare = 4;
 
-// The share that holds block tile f: shares are [c W / n, (c + 1) W / n).
+// The share that holds tile f: shares are [c W / n, (c + 1) W / n).
 __device__ __forceinline__ int share_of(long long f, long long W, int n) {
   return static_cast<int>(((f + 1) * n - 1) / W);
 }
@@ -130,6 +127,352 @@ __device__ __forceinline__ Visible visible_of(int n, int window, int sinks) {
   return s;
 }
 
+// The sequences that a block looks at together, in shared memory.
+struct Seqs {
+  int len[kThreads], tiles[kThreads], slot[kThreads];
+  long long upto[kThreads];  // running sum of tiles
+  long long scan[kWarps];
+};
+
+// A place in the walk: tile f of the row that spans [lo, hi) of the batch's
+// tiles, row rs (K / V head, block of heads) of sequence j of the chunk.
+struct Cursor {
+  long long f, lo, hi;
+  int j, rs;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_kernel(const AttendParams p) {
+  using C = DecodeCfg<D>;
+  constexpr int KT = C::KT, STAGES = C::STAGES;
+  griddep_wait();
+  griddep_launch_dependents();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Seqs sq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q4 = lane & 3;  // row and column group of the matrix fragments
+  const int rows_per_seq = p.c.heads_kv * p.head_blocks;
+
+  // ---- the shares: tiles of every sequence, their sum and this warp's part
+  auto load_seq = [&](int b) -> int {  // length and tiles of sequence b, this thread's
+    int n = 0, slot = -1;
+    if (b < p.batch) {
+      slot = p.slots != nullptr ? p.slots[b] : b;
+      if (slot >= 0 && slot < p.c.slots)
+        n = min(max(p.c.lengths[slot], 0), p.c.max_pages * p.c.page_size);
+    }
+    sq.len[threadIdx.x] = n;
+    sq.slot[threadIdx.x] = slot;
+    const int tiles = (visible_of(n, p.window, p.sinks).count + KT - 1) / KT;
+    sq.tiles[threadIdx.x] = tiles;
+    return tiles;
+  };
+  // inclusive prefix sum over the block into sq.upto; returns the sum of all
+  auto scan = [&](long long x) -> long long {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) sq.scan[warp] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sq.scan[w];
+      all += sq.scan[w];
+    }
+    sq.upto[threadIdx.x] = x + before;
+    __syncthreads();
+    return all;
+  };
+  long long sum = 0, part = 0;  // tiles of one row per sequence
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    part = scan(load_seq(b0 + threadIdx.x));
+    sum += part;
+  }
+  const long long W = sum * rows_per_seq;
+  const long long want = (W + kMinShare - 1) / kMinShare;
+  const long long most = static_cast<long long>(gridDim.x) * kWarps;
+  const int shares = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+  // few shares: one or two warps of a block, so that they spread over the SMs
+  const int active = shares <= static_cast<int>(gridDim.x) ? 1 : shares <= 2 * static_cast<int>(gridDim.x) ? 2 : kWarps;
+  const int share = warp < active ? blockIdx.x * active + warp : shares;
+  const long long lo = share < shares ? share * W / shares : W;
+  const long long hi = share < shares ? (share + 1) * W / shares : W;
+  const bool keeper = blockIdx.x == 0 && p.tiles_upto != nullptr;  // leaves the plan to the joining kernel
+  if (keeper && threadIdx.x == 0) {
+    p.tiles_upto[0] = 0;
+    p.tiles_upto[p.batch + 1] = shares;
+  }
+
+  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
+  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
+
+  long long chunk_lo = 0;  // tile at which this chunk of sequences begins
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    if (p.batch > kThreads) part = scan(load_seq(b0 + threadIdx.x));  // else it is still there
+    if (keeper && b0 + static_cast<int>(threadIdx.x) < p.batch)
+      p.tiles_upto[b0 + threadIdx.x + 1] = chunk_lo / rows_per_seq + sq.upto[threadIdx.x];
+    // rows without keys belong to no share: the last block writes them
+    if (blockIdx.x == gridDim.x - 1) {
+      for (int j = 0; j < min(kThreads, p.batch - b0); ++j) {
+        if (sq.tiles[j] != 0) continue;
+        const int b = b0 + j;
+        for (int x = threadIdx.x; x < p.heads * (p.c.d / 8); x += kThreads) {
+          const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
+          *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
+          if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
+        }
+      }
+    }
+    const long long chunk_hi = chunk_lo + part * rows_per_seq;
+    const long long from = lo > chunk_lo ? lo : chunk_lo, end = hi < chunk_hi ? hi : chunk_hi;
+    if (from < end) {
+      // the row of tile `from`: the first sequence whose running sum passes it
+      Cursor at;
+      {
+        const long long fs = (from - chunk_lo) / rows_per_seq;
+        int a = 0, z = kThreads - 1;
+        while (a < z) {
+          const int mid = (a + z) / 2;
+          if (sq.upto[mid] > fs) z = mid;
+          else a = mid + 1;
+        }
+        at.j = a;
+        const int tiles = sq.tiles[a];
+        const long long seq_lo = chunk_lo + (sq.upto[a] - tiles) * rows_per_seq;
+        at.rs = static_cast<int>((from - seq_lo) / tiles);
+        at.lo = seq_lo + static_cast<long long>(at.rs) * tiles;
+        at.hi = at.lo + tiles;
+        at.f = from;
+      }
+      auto advance = [&](Cursor& c) {  // one tile on; c.f < end afterwards or the cursor is not used
+        if (++c.f < c.hi || c.f >= end) return;
+        if (++c.rs == rows_per_seq) {
+          c.rs = 0;
+          do ++c.j;
+          while (sq.tiles[c.j] == 0);
+        }
+        c.lo = c.hi;
+        c.hi += sq.tiles[c.j];
+      };
+
+      // K and V element offsets of this lane's key of the cursor's tile (lane & (KT - 1))
+      struct Key {
+        long long k, v;
+        bool live;
+      };
+      auto locate = [&](const Cursor& c) -> Key {
+        Key r{0, 0, false};
+        if (c.f >= end) return r;
+        const Visible vis = visible_of(sq.len[c.j], p.window, p.sinks);
+        const int u = static_cast<int>(c.f - c.lo) * KT + (lane & (KT - 1));
+        if (u < vis.count) {
+          const int j = vis.key(u);
+          const int cell = j / p.c.page_size;
+          const int page = p.c.table[static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell];
+          if (page >= 0 && page < p.c.pages) {
+            const int row = j - cell * p.c.page_size, hk = c.rs / p.head_blocks;
+            r.k = page * p.c.k_page + hk * p.c.k_head + row * p.c.k_row;
+            r.v = page * p.c.v_page + hk * p.c.v_head + row * p.c.v_row;
+            r.live = true;
+          }
+        }
+        return r;
+      };
+      // copies of one tile into a stage: whole rows, 16 bytes a lane
+      auto load = [&](int stage, const Key& r) {
+        constexpr int CH = D / 8, RPI = 32 / CH;  // pieces of a row, rows per step
+        const int c = lane % CH;
+        const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
+        const uint32_t live = __ballot_sync(0xffffffffu, r.live);
+        if (lane == 0) valid[stage] = live;
+        const bool col_ok = 8 * c < p.c.d;
+#pragma unroll
+        for (int s = 0; s < KT / RPI; ++s) {
+          const int row = s * RPI + lane / CH;
+          const long long ko = __shfl_sync(0xffffffffu, r.k, row);
+          const long long vo = __shfl_sync(0xffffffffu, r.v, row);
+          const bool ok = col_ok && ((live >> row) & 1u);
+          const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+          cp_async16(kdst + dst, p.k + (ok ? ko + 8 * c : 0), ok);
+          cp_async16(vdst + dst, p.v + (ok ? vo + 8 * c : 0), ok);
+        }
+      };
+
+      Cursor fill = at;
+      {
+        Key ahead[STAGES - 1];
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) {
+          ahead[s] = locate(fill);
+          advance(fill);
+        }
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) {
+          if (at.f + s < end) load(s, ahead[s]);
+          cp_async_commit();
+        }
+      }
+      Key next = locate(fill);
+
+      uint32_t qa[D / 16][4];     // Q as the A operand: rows g and g + 8
+      float o[D / 8][4];
+      float m[2], l[2];           // rows g, g + 8; l: this lane's part
+      bool begin = true;
+      int stage = 0;
+      while (at.f < end) {
+        // the next free stage was read in the previous round
+        __syncwarp();
+        if (fill.f < end) load(stage == 0 ? STAGES - 1 : stage - 1, next);
+        cp_async_commit();
+        advance(fill);
+        next = locate(fill);
+        const int hk = at.rs / p.head_blocks, hb = at.rs - hk * p.head_blocks;
+        const int h0 = hk * p.group + hb * 16;      // first query head of the row
+        const int hn = min(16, p.group - hb * 16);  // its query heads
+        const int b = b0 + at.j;
+        if (begin) {  // zero past the row's heads and past d
+          const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int r = g + 8 * (u & 1), col = 16 * kk + 8 * (u >> 1) + 2 * q4;
+              qa[kk][u] = r < hn && col < p.c.d
+                              ? *reinterpret_cast<const uint32_t*>(q0 + r * p.q_head + col)
+                              : 0u;
+            }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[i][u] = 0.f;
+          m[0] = m[1] = -INFINITY;
+          l[0] = l[1] = 0.f;
+          begin = false;
+        }
+        cp_async_wait<STAGES - 1>();
+        __syncwarp();
+        const uint32_t kbase = ring + stage * C::STAGE, vbase = kbase + KT * C::ROW;
+        const uint32_t live = valid[stage];
+        float s[KT / 8][4];
+#pragma unroll
+        for (int i = 0; i < KT / 8; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[i][u] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int kt = 0; kt < KT / 16; ++kt) {
+            uint32_t kb[4];
+            const int row = kt * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+            const int ch = 2 * kk + ((lane >> 3) & 1);
+            ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), kb);
+            mma16816(s[2 * kt], qa[kk], kb[0], kb[1]);
+            mma16816(s[2 * kt + 1], qa[kk], kb[2], kb[3]);
+          }
+        constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
+        if ((live & kAll) != kAll) {
+#pragma unroll
+          for (int i = 0; i < KT / 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              s[i][u] = (live >> (8 * i + 2 * q4 + (u & 1))) & 1u ? s[i][u] : -INFINITY;
+        }
+        float alpha[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < KT / 8; ++i) mx = fmax3(mx, s[i][2 * r], s[i][2 * r + 1]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float m_new = fmaxf(m[r], mx * p.scale_log2);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          alpha[r] = fast_exp2(m[r] - ref);
+          m[r] = m_new;
+          float rs = 0.f;
+#pragma unroll
+          for (int i = 0; i < KT / 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float e = fast_exp2(fmaf(s[i][2 * r + u], p.scale_log2, -ref));
+              s[i][2 * r + u] = e;
+              rs += e;
+            }
+          l[r] = l[r] * alpha[r] + rs;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= alpha[0];
+            o[i][1] *= alpha[0];
+            o[i][2] *= alpha[1];
+            o[i][3] *= alpha[1];
+          }
+        }
+        // P is rounded to bf16 for the second product, as in the other attention
+        // kernels; the row sum keeps the unrounded values
+#pragma unroll
+        for (int kt = 0; kt < KT / 16; ++kt) {
+          const uint32_t pa[4] = {pack_bf16(s[2 * kt][0], s[2 * kt][1]), pack_bf16(s[2 * kt][2], s[2 * kt][3]),
+                                  pack_bf16(s[2 * kt + 1][0], s[2 * kt + 1][1]),
+                                  pack_bf16(s[2 * kt + 1][2], s[2 * kt + 1][3])};
+#pragma unroll
+          for (int dd = 0; dd < D / 16; ++dd) {
+            uint32_t vb[4];
+            const int row = kt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+            const int ch = 2 * dd + (lane >> 4);
+            ldsm_x4_trans(vbase + row * C::ROW + ((ch ^ (row & 7)) << 4), vb);
+            mma16816(o[2 * dd], pa, vb[0], vb[1]);
+            mma16816(o[2 * dd + 1], pa, vb[2], vb[3]);
+          }
+        }
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+
+        const long long f1 = at.f + 1;
+        if (f1 == at.hi || f1 == end) {
+          // the row ends, or the share: the whole row goes to O and LSE, a part of
+          // it to the share's partial results, index 1 where the row begins in
+          // this share, 0 where it goes on
+          const bool begins = at.lo >= lo, whole = begins && f1 == at.hi;
+          const long long pr = (2ll * share + (begins ? 1 : 0)) * 16;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            const int row = g + 8 * r;
+            if (row >= hn) continue;
+            if (whole) {
+              const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+              __nv_bfloat16* dst = p.o + b * p.o_batch + (h0 + row) * p.o_head + 2 * q4;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                if (8 * i < p.c.d)
+                  *reinterpret_cast<uint32_t*>(dst + 8 * i) = pack_bf16(o[i][2 * r] * inv, o[i][2 * r + 1] * inv);
+              if (q4 == 0)
+                p.lse[static_cast<long long>(b) * p.heads + h0 + row] =
+                    l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+            } else {
+              float* dst = p.part_acc + (pr + row) * D + 2 * q4;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+              if (q4 == 0) p.part_stat[pr + row] = make_float2(m[r], l[r]);
+            }
+          }
+          begin = true;
+        }
+        advance(at);
+      }
+      cp_async_wait<0>();
+    }
+    chunk_lo = chunk_hi;
+    if (p.batch > kThreads) __syncthreads();  // the next chunk overwrites the sequences
+  }
+}
+
 // Eight columns of query head h of sequence b: O = out / sum, LSE = ln2 (m + log2 sum).
 __device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, int col, float m, float sum,
                                           const float (&out)[8]) {
@@ -141,368 +484,9 @@ __device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, i
     p.lse[static_cast<long long>(b) * p.heads + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// Block tiles [t0, t1) of one row: sequence b in `slot` with n keys, K / V head
-// hk, block hb of its query heads.  The whole row (t0 = 0, t1 = row_tiles) is
-// written to O and LSE, a part of it to the share's partial results: index 1
-// where the row begins in this share, 0 where it goes on.
-template <int D>
-__device__ __forceinline__ void attend_segment(const AttendParams& p, uint8_t* smem, uint32_t ring,
-                                               uint32_t* valid, int b, int slot, int n, int hk, int hb,
-                                               int t0, int t1, int row_tiles, int share) {
-  using C = DecodeCfg<D>;
-  constexpr int KT = C::KT, STAGES = C::STAGES;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, q4 = lane & 3;  // row and column group of the matrix fragments
-  const int h0 = hk * p.group + hb * 16;               // first query head
-  const int hn = min(16, p.group - hb * 16);           // query heads
-  const Visible vis = visible_of(n, p.window, p.sinks);
-  const int tiles = min(t1 * kWarps, (vis.count + KT - 1) / KT);  // end, in warp tiles
-  const int32_t* pages = p.c.table + static_cast<long long>(slot) * p.c.max_pages;
-
-  // Q as the A operand: rows g and g + 8, zero past the block's heads and past d
-  uint32_t qa[D / 16][4];
-  {
-    const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = g + 8 * (u & 1), col = 16 * kk + 8 * (u >> 1) + 2 * q4;
-        qa[kk][u] = r < hn && col < p.c.d
-                        ? *reinterpret_cast<const uint32_t*>(q0 + r * p.q_head + col)
-                        : 0u;
-      }
-  }
-
-  // K and V element offsets of this lane's key of a tile (lane & (KT - 1)), -1: none
-  struct Row {
-    long long k, v;
-    bool live;
-  };
-  auto locate = [&](int tile) -> Row {
-    Row r{0, 0, false};
-    const int u = tile * KT + (lane & (KT - 1));
-    if (u < vis.count) {
-      const int j = vis.key(u);
-      const int cell = j / p.c.page_size;
-      const int page = pages[cell];
-      if (page >= 0 && page < p.c.pages) {
-        const int row = j - cell * p.c.page_size;
-        r.k = page * p.c.k_page + hk * p.c.k_head + row * p.c.k_row;
-        r.v = page * p.c.v_page + hk * p.c.v_head + row * p.c.v_row;
-        r.live = true;
-      }
-    }
-    return r;
-  };
-  // copies of one tile into a stage: whole rows, 16 bytes a lane
-  auto load = [&](int stage, const Row& r) {
-    constexpr int CH = D / 8, RPI = 32 / CH > 0 ? 32 / CH : 1;  // pieces of a row, rows per step
-    const int c = lane % CH;
-    const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
-    const uint32_t live = __ballot_sync(0xffffffffu, r.live);
-    if (lane == 0) valid[stage] = live;
-    const bool col_ok = 8 * c < p.c.d;
-#pragma unroll
-    for (int s = 0; s < KT / RPI; ++s) {
-      const int row = s * RPI + lane / CH;
-      const long long ko = __shfl_sync(0xffffffffu, r.k, row);
-      const long long vo = __shfl_sync(0xffffffffu, r.v, row);
-      const bool ok = col_ok && ((live >> row) & 1u);
-      const uint32_t at = row * C::ROW + ((c ^ (row & 7)) << 4);
-      cp_async16(kdst + at, p.k + (ok ? ko + 8 * c : 0), ok);
-      cp_async16(vdst + at, p.v + (ok ? vo + 8 * c : 0), ok);
-    }
-  };
-
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) o[i][u] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8; l: this lane's part
-
-  // tiles t0 kWarps + warp, + kWarps, ...
-  int fill = t0 * kWarps + warp;
-  {
-    Row ahead[STAGES - 1];
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) ahead[s] = locate(fill + s * kWarps);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      if (fill < tiles) load(s, ahead[s]);
-      cp_async_commit();
-      fill += kWarps;
-    }
-  }
-  Row next = locate(fill);
-  int stage = 0;
-  for (int tile = t0 * kWarps + warp; tile < tiles; tile += kWarps) {
-    // the next free stage was read in the previous round
-    __syncwarp();
-    {
-      const int into = stage == 0 ? STAGES - 1 : stage - 1;
-      if (fill < tiles) load(into, next);
-      cp_async_commit();
-      fill += kWarps;
-      next = locate(fill);
-    }
-    cp_async_wait<STAGES - 1>();
-    __syncwarp();
-    const uint32_t kbase = ring + stage * C::STAGE, vbase = kbase + KT * C::ROW;
-    const uint32_t live = valid[stage];
-    float s[KT / 8][4];
-#pragma unroll
-    for (int i = 0; i < KT / 8; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) s[i][u] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-      for (int kt = 0; kt < KT / 16; ++kt) {
-        uint32_t kb[4];
-        const int row = kt * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
-        const int ch = 2 * kk + ((lane >> 3) & 1);
-        ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), kb);
-        mma16816(s[2 * kt], qa[kk], kb[0], kb[1]);
-        mma16816(s[2 * kt + 1], qa[kk], kb[2], kb[3]);
-      }
-    constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
-    if ((live & kAll) != kAll) {
-#pragma unroll
-      for (int i = 0; i < KT / 8; ++i)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (((live >> (8 * i + 2 * q4 + (u & 1))) & 1u) == 0u) s[i][u] = -INFINITY;
-    }
-    float alpha[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < KT / 8; ++i) mx = fmax3(mx, s[i][2 * r], s[i][2 * r + 1]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float m_new = fmaxf(m[r], mx * p.scale_log2);
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
-      alpha[r] = fast_exp2(m[r] - ref);
-      m[r] = m_new;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < KT / 8; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float e = fast_exp2(fmaf(s[i][2 * r + u], p.scale_log2, -ref));
-          s[i][2 * r + u] = e;
-          sum += e;
-        }
-      l[r] = l[r] * alpha[r] + sum;
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= alpha[0];
-        o[i][1] *= alpha[0];
-        o[i][2] *= alpha[1];
-        o[i][3] *= alpha[1];
-      }
-    }
-    // P is rounded to bf16 for the second product, as in the other attention
-    // kernels; the row sum keeps the unrounded values
-#pragma unroll
-    for (int kt = 0; kt < KT / 16; ++kt) {
-      const uint32_t pa[4] = {pack_bf16(s[2 * kt][0], s[2 * kt][1]), pack_bf16(s[2 * kt][2], s[2 * kt][3]),
-                              pack_bf16(s[2 * kt + 1][0], s[2 * kt + 1][1]),
-                              pack_bf16(s[2 * kt + 1][2], s[2 * kt + 1][3])};
-#pragma unroll
-      for (int dd = 0; dd < D / 16; ++dd) {
-        uint32_t vb[4];
-        const int row = kt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-        const int ch = 2 * dd + (lane >> 4);
-        ldsm_x4_trans(vbase + row * C::ROW + ((ch ^ (row & 7)) << 4), vb);
-        mma16816(o[2 * dd], pa, vb[0], vb[1]);
-        mma16816(o[2 * dd + 1], pa, vb[2], vb[3]);
-      }
-    }
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-  }
-  cp_async_wait<0>();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-  }
-
-  // The warps' parts meet in the (now idle) ring: [warp][16 rows] statistics
-  // and [warp][16][D] fp32 sums.
-  __syncthreads();
-  float2* stat = reinterpret_cast<float2*>(smem);
-  float* acc = reinterpret_cast<float*>(smem + kWarps * 16 * sizeof(float2));
-  if (q4 == 0) {
-    stat[warp * 16 + g] = make_float2(m[0], l[0]);
-    stat[warp * 16 + g + 8] = make_float2(m[1], l[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    float* a = acc + (warp * 16 + g) * D + 8 * i + 2 * q4;
-    *reinterpret_cast<float2*>(a) = make_float2(o[i][0], o[i][1]);
-    *reinterpret_cast<float2*>(a + 8 * D) = make_float2(o[i][2], o[i][3]);
-  }
-  __syncthreads();
-  const bool whole = t0 == 0 && t1 == row_tiles;
-  const long long part = 2ll * share + (t0 == 0 ? 1 : 0);
-  for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
-    const int r = x / (D / 8), col = 8 * (x % (D / 8));
-    if (col >= p.c.d) continue;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * 16 + r].x);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float sum = 0.f, out[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 st = stat[w * 16 + r];
-      const float f = fast_exp2(st.x - ref);
-      sum += f * st.y;
-      const float4* a = reinterpret_cast<const float4*>(acc + (w * 16 + r) * D + col);
-      const float4 a0 = a[0], a1 = a[1];
-      const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = fmaf(f, v[e], out[e]);
-    }
-    if (whole) {
-      write_row(p, b, h0 + r, col, mm, sum, out);
-    } else {
-      float4* a = reinterpret_cast<float4*>(p.part_acc + (part * 16 + r) * D + col);
-      a[0] = make_float4(out[0], out[1], out[2], out[3]);
-      a[1] = make_float4(out[4], out[5], out[6], out[7]);
-      if (col == 0) p.part_stat[part * 16 + r] = make_float2(mm, sum);
-    }
-  }
-  __syncthreads();  // the next segment fills the ring again
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_kernel(const AttendParams p) {
-  using C = DecodeCfg<D>;
-  constexpr int STAGES = C::STAGES;
-  griddep_wait();
-  griddep_launch_dependents();
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- the shares: block tiles of every sequence, their sum and this block's part
-  __shared__ int s_len[kThreads], s_tiles[kThreads], s_slot[kThreads];
-  __shared__ long long s_upto[kThreads];
-  __shared__ long long s_scan[kWarps];
-  const int rows_per_seq = p.c.heads_kv * p.head_blocks;
-  auto load_seq = [&](int b) {  // length and block tiles of sequence b, this thread's
-    int n = 0, slot = -1;
-    if (b < p.batch) {
-      slot = p.slots != nullptr ? p.slots[b] : b;
-      if (slot >= 0 && slot < p.c.slots)
-        n = min(max(p.c.lengths[slot], 0), p.c.max_pages * p.c.page_size);
-    }
-    s_len[threadIdx.x] = n;
-    s_slot[threadIdx.x] = slot;
-    s_tiles[threadIdx.x] = (visible_of(n, p.window, p.sinks).count + C::BT - 1) / C::BT;
-    return static_cast<long long>(s_tiles[threadIdx.x]);
-  };
-  // inclusive prefix sum over the block; *total: the sum of all
-  auto scan = [&](long long x, long long* total) {
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      all += s_scan[w];
-    }
-    *total = all;
-    return x + before;
-  };
-  long long sum = 0;  // block tiles of one row per sequence
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    long long part = 0;
-    scan(load_seq(b0 + threadIdx.x), &part);
-    sum += part;
-  }
-  const long long W = sum * rows_per_seq;
-  const long long want = (W + kMinShare - 1) / kMinShare;
-  const int shares = want < 1 ? 1 : want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
-  const bool keeper = blockIdx.x == 0 && p.tiles_upto != nullptr;  // leaves the plan to the joining kernel
-  if (keeper && threadIdx.x == 0) p.tiles_upto[p.batch + 1] = shares;
-  const int share = blockIdx.x;
-  const long long lo = share < shares ? share * W / shares : W;
-  const long long hi = share < shares ? (share + 1) * W / shares : W;
-
-  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
-  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
-
-  long long chunk_lo = 0;  // block tile at which this chunk of sequences begins
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    long long part = 0;
-    const long long mine = load_seq(b0 + threadIdx.x);
-    const long long upto = scan(mine, &part);
-    s_upto[threadIdx.x] = upto;
-    if (keeper && b0 + static_cast<int>(threadIdx.x) < p.batch) {
-      p.tiles_upto[b0 + threadIdx.x + 1] = chunk_lo / rows_per_seq + upto;
-      if (b0 + threadIdx.x == 0) p.tiles_upto[0] = 0;
-    }
-    // rows without keys belong to no share: block 0 writes them
-    __syncthreads();
-    if (blockIdx.x == 0) {
-      for (int j = 0; j < min(kThreads, p.batch - b0); ++j) {
-        if (s_tiles[j] != 0) continue;
-        const int b = b0 + j;
-        for (int x = threadIdx.x; x < p.heads * (p.c.d / 8); x += kThreads) {
-          const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
-          *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
-          if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
-        }
-      }
-    }
-    const long long chunk_hi = chunk_lo + part * rows_per_seq;
-    const long long from = lo > chunk_lo ? lo : chunk_lo, end = hi < chunk_hi ? hi : chunk_hi;
-    for (long long f = from; f < end;) {
-      // the sequence of block tile f: the first whose running sum passes it
-      const long long fs = (f - chunk_lo) / rows_per_seq;
-      int bl = 0;
-      {
-        int a = 0, z = kThreads - 1;
-        while (a < z) {
-          const int mid = (a + z) / 2;
-          if (s_upto[mid] > fs) z = mid;
-          else a = mid + 1;
-        }
-        bl = a;
-      }
-      const int row_tiles = s_tiles[bl];
-      const long long seq_lo = chunk_lo + (s_upto[bl] - row_tiles) * rows_per_seq;
-      const int rs = static_cast<int>((f - seq_lo) / row_tiles);  // (K / V head, block of heads)
-      const long long row_lo = seq_lo + static_cast<long long>(rs) * row_tiles;
-      const int t0 = static_cast<int>(f - row_lo);
-      const int t1 = static_cast<int>((end - row_lo < row_tiles ? end - row_lo : row_tiles));
-      f = row_lo + t1;
-      attend_segment<D>(p, smem, ring, valid, b0 + bl, s_slot[bl], s_len[bl], rs / p.head_blocks,
-                        rs % p.head_blocks, t0, t1, row_tiles, share);
-    }
-    chunk_lo = chunk_hi;
-    __syncthreads();  // the next chunk overwrites the sequences
-  }
-}
-
 // Joins the parts of rows that were cut: a block per (sequence, query head),
 // D / 8 threads over the columns, kJoinThreads / (D / 8) groups over the parts.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
@@ -563,8 +547,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
 
 // Grid and workspace of a call, from what the host knows: the longest that a
 // sequence may see.  One block per resident slot of the GPU, fewer where the
-// batch cannot have that many block tiles; no row can be cut, and none has to
-// be joined, where none can have more than one.
+// batch cannot have a share for one warp of each; no row can be cut, and none
+// has to be joined, where none can have more than one tile.
 struct Plan {
   long long grid;
   bool cut;
@@ -573,25 +557,26 @@ struct Plan {
 
 Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const int D = c.d <= 64 ? 64 : c.d <= 128 ? 128 : 256;
-  const int BT = D == 64 ? DecodeCfg<64>::BT : D == 128 ? DecodeCfg<128>::BT : DecodeCfg<256>::BT;
+  const int KT = D == 64 ? DecodeCfg<64>::KT : D == 128 ? DecodeCfg<128>::KT : DecodeCfg<256>::KT;
   const int per_sm = D == 256 ? DecodeCfg<256>::MIN_BLOCKS : DecodeCfg<128>::MIN_BLOCKS;
   long long most = static_cast<long long>(c.max_pages) * c.page_size;
   if (window > 0 && static_cast<long long>(window) + sinks < most) most = static_cast<long long>(window) + sinks;
-  const long long tiles = (most + BT - 1) / BT;
+  const long long tiles = (most + KT - 1) / KT;
   const long long rows = static_cast<long long>(batch) * c.heads_kv * ((heads / c.heads_kv + 15) / 16);
   Plan p;
-  p.grid = rows * tiles < 148ll * per_sm ? rows * tiles : 148ll * per_sm;
+  const long long blocks = (rows * tiles + kMinShare - 1) / kMinShare;  // one warp each
+  p.grid = blocks < 148ll * per_sm ? blocks : 148ll * per_sm;
   p.cut = tiles > 1;
   p.off_stat = ((static_cast<size_t>(batch) + 2) * 8 + 255) / 256 * 256;
-  p.off_acc = p.off_stat + static_cast<size_t>(p.grid) * 2 * 16 * sizeof(float2);
-  p.bytes = p.cut ? p.off_acc + static_cast<size_t>(p.grid) * 2 * 16 * D * sizeof(float) : 0;
+  const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
+  p.off_acc = p.off_stat + parts * sizeof(float2);
+  p.bytes = p.cut ? p.off_acc + parts * D * sizeof(float) : 0;
   return p;
 }
 
 template <int D>
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t stream) {
   using C = DecodeCfg<D>;
-  static_assert(kWarps * 16 * (8 + D * 4) <= C::OFF_VALID, "the warps' parts fit the ring");
   auto kern = attend_kernel<D>;
   static OncePerContext prepared;
   const cudaError_t e = prepared.run([&]() -> cudaError_t {
