@@ -183,8 +183,13 @@ def _check(code, where):
 
 
 def _stream_ptr(device):
+    """The current stream's handle on `device` (a torch.device, an index or None)."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    index = getattr(device, "index", device)
+    if index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    # the same handle without a Stream object around it (0.1 us for 2 us)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t):
@@ -207,15 +212,20 @@ def _check_qkv(*ts):
             raise ValueError("q, k, v (and o, dout) must share shape and device")
 
 
-def _masks(seqlens, block_mask, device):
+def _array(x, dtype, device):
+    """x (a tensor, an array or a list) as a contiguous tensor on the device."""
     import torch
-    sl = None
-    if seqlens is not None:
-        sl = torch.as_tensor(seqlens, dtype=torch.int32, device=device).contiguous()
-    bm = None
-    if block_mask is not None:
-        bm = torch.as_tensor(block_mask, dtype=torch.uint8, device=device).contiguous()
-    return sl, bm
+    if isinstance(x, torch.Tensor) and x.dtype is dtype and x.device == device and x.is_contiguous():
+        return x
+    return torch.as_tensor(x, dtype=dtype, device=device).contiguous()
+
+
+def _masks(seqlens, block_mask, device):
+    if seqlens is None and block_mask is None:
+        return None, None
+    import torch
+    return (None if seqlens is None else _array(seqlens, torch.int32, device),
+            None if block_mask is None else _array(block_mask, torch.uint8, device))
 
 
 @_nvtx("fa.forward")
@@ -353,14 +363,15 @@ def wait_timeout_probe(device=None):
 def _strides(t, layout):
     if t is None:
         return Strides(0, 0, 0)
-    if t.stride(-1) != 1:
+    s = t.stride()
+    if s[-1] != 1:
         raise ValueError("the head dimension must be contiguous")
     if layout == "bhsd":
-        return Strides(t.stride(0), t.stride(1), t.stride(2))
+        return Strides(s[0], s[1], s[2])
     if layout == "bshd":
-        return Strides(t.stride(0), t.stride(2), t.stride(1))
+        return Strides(s[0], s[2], s[1])
     if layout == "thd":
-        return Strides(0, t.stride(1), t.stride(0))
+        return Strides(0, s[1], s[0])
     raise ValueError(f"unknown layout {layout!r}")
 
 
@@ -384,13 +395,14 @@ def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, 
     if layout not in ("bhsd", "bshd", "thd"):
         raise ValueError(f"unknown layout {layout!r}")
     want_dim = 3 if layout == "thd" else 4
+    device, shape_q, shape_k = q.device, q.shape, k.shape
     for name, t in tensors.items():
         if t.dim() != want_dim:
             raise ValueError(f"{name}: a {want_dim}-D tensor is expected for layout {layout!r}")
-        if not t.is_cuda or t.dtype != torch.bfloat16 or t.device != q.device:
+        if not t.is_cuda or t.dtype is not torch.bfloat16 or t.device != device:
             raise ValueError(f"{name}: bfloat16 on the device of q is expected")
         ref = q if name in _Q_SIDE else k
-        if t.shape != ref.shape:
+        if t.shape != (shape_q if name in _Q_SIDE else shape_k):
             raise ValueError(f"{name}: shape {tuple(t.shape)} differs from "
                              f"{'q' if name in _Q_SIDE else 'k'} {tuple(ref.shape)}")
     Bq, Nq, H, d = _dims(q, layout)
@@ -404,8 +416,8 @@ def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, 
     if layout == "thd":
         if cu_seqlens_q is None or cu_seqlens_k is None:
             raise ValueError("the packed layout needs cu_seqlens_q and cu_seqlens_k")
-        cq = torch.as_tensor(cu_seqlens_q, dtype=torch.int32, device=q.device).contiguous()
-        ck = torch.as_tensor(cu_seqlens_k, dtype=torch.int32, device=q.device).contiguous()
+        cq = _array(cu_seqlens_q, torch.int32, device)
+        ck = _array(cu_seqlens_k, torch.int32, device)
         keep += [cq, ck]
         a.batch = cq.numel() - 1
         a.cu_seqlens_q, a.cu_seqlens_k = cq.data_ptr(), ck.data_ptr()

@@ -40,7 +40,7 @@ class PagedCache:
         self.k, self.v, self.table, self.lengths, self.refs = k, v, table, lengths, refs
         self.layers, self.pages, self.heads_kv, self.page_size, self.head_dim = k.shape
         self.slots, self.max_pages = table.shape
-        self.device = k.device
+        self.device, self._row = k.device, (self.heads_kv, self.head_dim)
         a = _fa.CacheDesc()
         a.layers, a.pages, a.page_size = self.layers, self.pages, self.page_size
         a.heads_kv, a.head_dim = self.heads_kv, self.head_dim
@@ -51,7 +51,8 @@ class PagedCache:
         a.vs = _fa.Strides(v.stride(1), v.stride(2), v.stride(3))
         a.table, a.lengths, a.refs = table.data_ptr(), lengths.data_ptr(), refs.data_ptr()
         self._desc, self._ref = a, ctypes.byref(a)
-        self._lib = _fa.library()
+        self._lib, self._torch, self._index = _fa.library(), torch, k.get_device()
+        self._sizes = {}
         if self._lib.fa_cache_workspace_size(self._ref, 0) == 0:
             raise ValueError("the cache's sizes, strides or alignment are not supported (fa.h)")
 
@@ -64,39 +65,43 @@ class PagedCache:
         ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
         return cls(*kv, ints(slots, max_pages).fill_(-1), ints(slots), ints(pages))
 
-    def _ints(self, name, t, n=None):
-        import torch
-        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.device or not t.is_contiguous():
+    def _ints(self, name, t, n):
+        if (t.dtype is not self._torch.int32 or t.dim() != 1 or t.get_device() != self._index
+                or not t.is_contiguous()):
             raise ValueError(f"{name}: a contiguous 1-D int32 tensor on the cache's device is expected")
-        if n is not None and t.shape[0] != n:
+        if t.shape[0] != n:
             raise ValueError(f"{name}: {n} entries are expected, got {t.shape[0]}")
         return t.data_ptr()
 
-    def _workspace(self, n):
-        import torch
-        size = self._lib.fa_cache_workspace_size(self._ref, n)
-        return torch.empty(size, dtype=torch.uint8, device=self.device), size
+    def _empty(self, shape, dtype):
+        return self._torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _call(self, name, *args):
+    def _workspace(self, n):
+        size = self._sizes.get(n)
+        if size is None:  # a function of the cache's sizes and n alone
+            size = self._sizes[n] = self._lib.fa_cache_workspace_size(self._ref, n)
+        return self._empty(size, self._torch.uint8), size
+
+    def _call(self, fn, *args):
         """The C call on the cache's device and that device's current stream."""
-        import torch
-        if torch.cuda.current_device() == self.device.index:
-            code = getattr(self._lib, name)(self._ref, *args, _fa._stream_ptr(self.device))
+        c = self._torch._C
+        if c._cuda_getDevice() == self._index:
+            code = fn(self._ref, *args, c._cuda_getCurrentRawStream(self._index))
         else:
-            with torch.cuda.device(self.device):
-                code = getattr(self._lib, name)(self._ref, *args, _fa._stream_ptr(self.device))
-        _fa._check(code, name)
+            with self._torch.cuda.device(self._index):
+                code = fn(self._ref, *args, c._cuda_getCurrentRawStream(self._index))
+        if code:
+            _fa._check(code, fn.__name__)
 
     @_fa._nvtx("fa.cache.extend")
     def extend(self, slots, tokens):
         """Grows slots[i] by tokens[i]; returns start (int32 [n]), each entry's
         first new position, -1 where it was not granted (fa_cache_extend)."""
-        import torch
         n = slots.shape[0]
-        start = torch.empty(n, dtype=torch.int32, device=self.device)
+        start = self._empty(n, self._torch.int32)
         ws, size = self._workspace(n)
-        self._call("fa_cache_extend", self._ints("slots", slots), self._ints("tokens", tokens, n), n,
-                   start.data_ptr(), ws.data_ptr(), size)
+        self._call(self._lib.fa_cache_extend, self._ints("slots", slots, n),
+                   self._ints("tokens", tokens, n), n, start.data_ptr(), ws.data_ptr(), size)
         return start
 
     @_fa._nvtx("fa.cache.write")
@@ -104,19 +109,20 @@ class PagedCache:
         """Writes k, v (bf16 [T, heads_kv, d]) of one layer to the positions
         start[i], start[i] + 1, ... of slots[i]: one row per entry, or with
         cu_seqlens (int32 [n + 1]) rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1."""
-        import torch
-        n = slots.shape[0]
-        for name, t in (("k", k), ("v", v)):
-            if t.dim() != 3 or t.shape[1:] != (self.heads_kv, self.head_dim) or t.shape != k.shape:
-                raise ValueError(f"{name}: [T, {self.heads_kv}, {self.head_dim}] is expected")
-            if t.dtype != torch.bfloat16 or t.device != self.device or t.stride(2) != 1:
-                raise ValueError(f"{name}: bfloat16 on the cache's device, d contiguous, is expected")
-        cu = None if cu_seqlens is None else self._ints("cu_seqlens", cu_seqlens, n + 1)
-        if cu is None and k.shape[0] != n:
+        n, bf16 = slots.shape[0], self._torch.bfloat16
+        shape = k.shape
+        if len(shape) != 3 or shape[1:] != self._row or v.shape != shape:
+            raise ValueError(f"k, v: [T, {self.heads_kv}, {self.head_dim}] of one shape are expected")
+        sk, sv = k.stride(), v.stride()
+        if (k.dtype is not bf16 or v.dtype is not bf16 or k.get_device() != self._index
+                or v.get_device() != self._index or sk[2] != 1 or sv[2] != 1):
+            raise ValueError("k, v: bfloat16 on the cache's device, d contiguous, are expected")
+        if cu_seqlens is None and shape[0] != n:
             raise ValueError("write: one row per slot is expected without cu_seqlens")
-        self._call("fa_cache_write", layer, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                   v.stride(0), v.stride(1), self._ints("slots", slots),
-                   self._ints("start", start, n), cu, n, k.shape[0])
+        cu = None if cu_seqlens is None else self._ints("cu_seqlens", cu_seqlens, n + 1)
+        self._call(self._lib.fa_cache_write, layer, k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0],
+                   sv[1], self._ints("slots", slots, n), self._ints("start", start, n), cu, n,
+                   shape[0])
 
     @_fa._nvtx("fa.cache.attend")
     def attend(self, layer, q, slots=None, scale=None, window=0, sinks=0, out=None, lse=None):
@@ -124,32 +130,37 @@ class PagedCache:
         its slot (slots int32 [B]; None: slot b for query b), with a window and
         first tokens as in forward_general.  The newest token has to be in the
         cache.  LSE: fp32 [B, H]."""
-        import torch
-        if q.dim() != 3 or q.shape[2] != self.head_dim:
+        torch = self._torch
+        shape, sq = q.shape, q.stride()
+        if len(shape) != 3 or shape[2] != self.head_dim:
             raise ValueError(f"q: [B, H, {self.head_dim}] is expected")
-        B, H, d = q.shape
+        B, H, d = shape
         if H < 1 or H % self.heads_kv:
             raise ValueError("q's heads must be a multiple of the cache's")
         if out is None:
-            out = torch.empty((B, H, d), dtype=torch.bfloat16, device=self.device)
+            out = self._empty(shape, torch.bfloat16)
+        so = out.stride()
         if lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=self.device)
-        elif (lse.shape != (B, H) or lse.dtype != torch.float32 or lse.device != self.device
+            lse = self._empty((B, H), torch.float32)
+        elif (lse.shape != (B, H) or lse.dtype is not torch.float32 or lse.get_device() != self._index
               or not lse.is_contiguous()):
             raise ValueError(f"lse: contiguous float32 {(B, H)} on the cache's device is expected")
-        for name, t in (("q", q), ("out", out)):
-            if (t.dtype != torch.bfloat16 or t.device != self.device or t.shape != q.shape
-                    or t.stride(2) != 1):
-                raise ValueError(f"{name}: bfloat16 {tuple(q.shape)} on the cache's device, d "
+        for name, t, st in (("q", q, sq), ("out", out, so)):
+            if (t.dtype is not torch.bfloat16 or t.get_device() != self._index or t.shape != shape
+                    or st[2] != 1):
+                raise ValueError(f"{name}: bfloat16 {tuple(shape)} on the cache's device, d "
                                  "contiguous, is expected")
         window, sinks = _fa._window(window, sinks)
-        size = self._lib.fa_cache_attend_workspace_size(self._ref, B, H, window, sinks)
-        ws = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
-        self._call("fa_cache_attend", layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                   q.stride(0), q.stride(1), out.stride(0), out.stride(1),
+        key = (B, H, window, sinks)
+        size = self._sizes.get(key)
+        if size is None:  # a function of the cache's sizes and these alone
+            size = self._sizes[key] = self._lib.fa_cache_attend_workspace_size(self._ref, *key)
+        ws = self._empty(size, torch.uint8) if size else None
+        self._call(self._lib.fa_cache_attend, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                   sq[0], sq[1], so[0], so[1],
                    None if slots is None else self._ints("slots", slots, B), B, H,
-                   d ** -0.5 if scale is None else float(scale), window, sinks,
-                   None if ws is None else ws.data_ptr(), size)
+                   d ** -0.5 if scale is None else scale, window, sinks,
+                   ws.data_ptr() if size else None, size)
         return out, lse
 
     @_fa._nvtx("fa.cache.fork")
@@ -157,22 +168,22 @@ class PagedCache:
         """Slot dst[i] lets its pages go and shares src[i]'s (fa_cache_fork)."""
         n = src.shape[0]
         ws, size = self._workspace(n)
-        self._call("fa_cache_fork", self._ints("src", src), self._ints("dst", dst, n), n,
+        self._call(self._lib.fa_cache_fork, self._ints("src", src, n), self._ints("dst", dst, n), n,
                    ws.data_ptr(), size)
 
     @_fa._nvtx("fa.cache.free")
     def free(self, slots):
         """The slots let their pages go and become empty."""
-        self._call("fa_cache_free", self._ints("slots", slots), slots.shape[0])
+        n = slots.shape[0]
+        self._call(self._lib.fa_cache_free, self._ints("slots", slots, n), n)
 
     @_fa._nvtx("fa.cache.compact")
     def compact(self):
         """Moves the pages in use into the lowest numbers; returns how many there
         are (int32 [1], on the device)."""
-        import torch
-        used = torch.empty(1, dtype=torch.int32, device=self.device)
+        used = self._empty(1, self._torch.int32)
         ws, size = self._workspace(0)
-        self._call("fa_cache_compact", used.data_ptr(), ws.data_ptr(), size)
+        self._call(self._lib.fa_cache_compact, used.data_ptr(), ws.data_ptr(), size)
         return used
 
     @_fa._nvtx("fa.cache.copy_pages")
@@ -183,5 +194,5 @@ class PagedCache:
             raise ValueError("copy_pages: both caches on one device are expected")
         n = src.shape[0]
         ws, size = self._workspace(n)
-        self._call("fa_cache_copy_pages", None if source is None else source._ref,
-                   self._ints("src", src), self._ints("dst", dst, n), n, ws.data_ptr(), size)
+        self._call(self._lib.fa_cache_copy_pages, None if source is None else source._ref,
+                   self._ints("src", src, n), self._ints("dst", dst, n), n, ws.data_ptr(), size)
