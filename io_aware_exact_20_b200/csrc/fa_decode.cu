@@ -52,8 +52,7 @@ struct AttendParams {
   float scale_log2;  // softmax_scale * log2(e)
   int window, sinks;
   // partial results of the shares, null where no row can be cut
-  long long* tiles_upto;  // [batch + 1]: tiles of one row of every sequence before each, then
-                          // the number of shares
+  int2* cut_rows;         // [rows]: first and last share of each row
   float2* part_stat;      // [2 * shares][16]: maximum (log2 units), row sum
   float* part_acc;        // [2 * shares][16][D]
 };
@@ -127,6 +126,25 @@ __device__ __forceinline__ Visible visible_of(int n, int window, int sinks) {
   return s;
 }
 
+// Eight columns of query head h of sequence b: O = out / sum, LSE = ln2 (m + log2 sum).
+__device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, int col, float m, float sum,
+                                          const float (&out)[8]) {
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) =
+      make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
+                 pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
+  if (col == 0)
+    p.lse[static_cast<long long>(b) * p.heads + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// out += f * eight consecutive sums
+__device__ __forceinline__ void add_row8(float (&out)[8], float f, const float* a) {
+  const float4 a0 = reinterpret_cast<const float4*>(a)[0], a1 = reinterpret_cast<const float4*>(a)[1];
+  const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = fmaf(f, v[e], out[e]);
+}
+
 // The sequences that a block looks at together, in shared memory.
 struct Seqs {
   int len[kThreads], tiles[kThreads], slot[kThreads];
@@ -197,14 +215,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
   const int shares = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
   // few shares: one or two warps of a block, so that they spread over the SMs
   const int active = shares <= static_cast<int>(gridDim.x) ? 1 : shares <= 2 * static_cast<int>(gridDim.x) ? 2 : kWarps;
+  const long long blk0 = static_cast<long long>(blockIdx.x) * kWarps;
   const int share = warp < active ? blockIdx.x * active + warp : shares;
   const long long lo = share < shares ? share * W / shares : W;
   const long long hi = share < shares ? (share + 1) * W / shares : W;
-  const bool keeper = blockIdx.x == 0 && p.tiles_upto != nullptr;  // leaves the plan to the joining kernel
-  if (keeper && threadIdx.x == 0) {
-    p.tiles_upto[0] = 0;
-    p.tiles_upto[p.batch + 1] = shares;
-  }
 
   const uint32_t ring = smem_u32(smem) + warp * C::WARP;
   uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
@@ -212,8 +226,6 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
   long long chunk_lo = 0;  // tile at which this chunk of sequences begins
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     if (p.batch > kThreads) part = scan(load_seq(b0 + threadIdx.x));  // else it is still there
-    if (keeper && b0 + static_cast<int>(threadIdx.x) < p.batch)
-      p.tiles_upto[b0 + threadIdx.x + 1] = chunk_lo / rows_per_seq + sq.upto[threadIdx.x];
     // rows without keys belong to no share: the last block writes them
     if (blockIdx.x == gridDim.x - 1) {
       for (int j = 0; j < min(kThreads, p.batch - b0); ++j) {
@@ -224,6 +236,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
           if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
         }
+        if (p.cut_rows != nullptr)
+          for (int x = threadIdx.x; x < rows_per_seq; x += kThreads)
+            p.cut_rows[static_cast<long long>(b) * rows_per_seq + x] = make_int2(0, 0);
       }
     }
     const long long chunk_hi = chunk_lo + part * rows_per_seq;
@@ -258,26 +273,24 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         c.hi += sq.tiles[c.j];
       };
 
-      // K and V element offsets of this lane's key of the cursor's tile (lane & (KT - 1))
+      // Page and row of this lane's key (lane & (KT - 1)) of the cursor's tile,
+      // and the tile's K / V head.  The table cell is asked for a round before
+      // the copies need it, and nothing is computed from it until then: used at
+      // once, every round waits for the load (0.3 us).
       struct Key {
-        long long k, v;
-        bool live;
+        int page, row, hk;
       };
       auto locate = [&](const Cursor& c) -> Key {
-        Key r{0, 0, false};
+        Key r{-1, 0, 0};
         if (c.f >= end) return r;
         const Visible vis = visible_of(sq.len[c.j], p.window, p.sinks);
         const int u = static_cast<int>(c.f - c.lo) * KT + (lane & (KT - 1));
+        r.hk = c.rs / p.head_blocks;
         if (u < vis.count) {
           const int j = vis.key(u);
           const int cell = j / p.c.page_size;
-          const int page = p.c.table[static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell];
-          if (page >= 0 && page < p.c.pages) {
-            const int row = j - cell * p.c.page_size, hk = c.rs / p.head_blocks;
-            r.k = page * p.c.k_page + hk * p.c.k_head + row * p.c.k_row;
-            r.v = page * p.c.v_page + hk * p.c.v_head + row * p.c.v_row;
-            r.live = true;
-          }
+          r.row = j - cell * p.c.page_size;
+          r.page = p.c.table[static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell];
         }
         return r;
       };
@@ -286,14 +299,17 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         constexpr int CH = D / 8, RPI = 32 / CH;  // pieces of a row, rows per step
         const int c = lane % CH;
         const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
-        const uint32_t live = __ballot_sync(0xffffffffu, r.live);
+        const bool has = r.page >= 0 && r.page < p.c.pages;
+        const long long k0 = r.page * p.c.k_page + r.hk * p.c.k_head + r.row * p.c.k_row;
+        const long long v0 = r.page * p.c.v_page + r.hk * p.c.v_head + r.row * p.c.v_row;
+        const uint32_t live = __ballot_sync(0xffffffffu, has);
         if (lane == 0) valid[stage] = live;
         const bool col_ok = 8 * c < p.c.d;
 #pragma unroll
         for (int s = 0; s < KT / RPI; ++s) {
           const int row = s * RPI + lane / CH;
-          const long long ko = __shfl_sync(0xffffffffu, r.k, row);
-          const long long vo = __shfl_sync(0xffffffffu, r.v, row);
+          const long long ko = __shfl_sync(0xffffffffu, k0, row);
+          const long long vo = __shfl_sync(0xffffffffu, v0, row);
           const bool ok = col_ok && ((live >> row) & 1u);
           const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
           cp_async16(kdst + dst, p.k + (ok ? ko + 8 * c : 0), ok);
@@ -317,6 +333,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
       }
       Key next = locate(fill);
 
+      // whether the block's four shares lie in one row
+      const bool block_row = active == kWarps && shares >= blk0 + kWarps && at.lo <= blk0 * W / shares &&
+                             at.hi >= (blk0 + kWarps) * W / shares;
       uint32_t qa[D / 16][4];     // Q as the A operand: rows g and g + 8
       float o[D / 8][4];
       float m[2], l[2];           // rows g, g + 8; l: this lane's part
@@ -333,7 +352,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         const int h0 = hk * p.group + hb * 16;      // first query head of the row
         const int hn = min(16, p.group - hb * 16);  // its query heads
         const int b = b0 + at.j;
-        if (begin) {  // zero past the row's heads and past d
+        if (begin) {
+          // the joining kernel learns the row's shares from the one it begins in
+          if (p.cut_rows != nullptr && at.lo >= lo && lane == 0)
+            p.cut_rows[static_cast<long long>(b) * rows_per_seq + at.rs] =
+                make_int2(share, at.hi <= hi ? share : share_of(at.hi - 1, W, shares));
+          // Q: zero past the row's heads and past d
           const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -356,11 +380,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         __syncwarp();
         const uint32_t kbase = ring + stage * C::STAGE, vbase = kbase + KT * C::ROW;
         const uint32_t live = valid[stage];
-        float s[KT / 8][4];
+        // two sums per score, over the even and the odd steps: half the chain
+        float s[KT / 8][4], s1[KT / 8][4];
 #pragma unroll
         for (int i = 0; i < KT / 8; ++i)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) s[i][u] = 0.f;
+          for (int u = 0; u < 4; ++u) s[i][u] = s1[i][u] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -369,9 +394,13 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
             const int row = kt * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
             const int ch = 2 * kk + ((lane >> 3) & 1);
             ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), kb);
-            mma16816(s[2 * kt], qa[kk], kb[0], kb[1]);
-            mma16816(s[2 * kt + 1], qa[kk], kb[2], kb[3]);
+            mma16816(kk & 1 ? s1[2 * kt] : s[2 * kt], qa[kk], kb[0], kb[1]);
+            mma16816(kk & 1 ? s1[2 * kt + 1] : s[2 * kt + 1], qa[kk], kb[2], kb[3]);
           }
+#pragma unroll
+        for (int i = 0; i < KT / 8; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[i][u] += s1[i][u];
         constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
         if ((live & kAll) != kAll) {
 #pragma unroll
@@ -432,7 +461,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         stage = stage + 1 == STAGES ? 0 : stage + 1;
 
         const long long f1 = at.f + 1;
-        if (f1 == at.hi || f1 == end) {
+        if (block_row && f1 == end) {
+          // all of the block's shares are parts of this row: they meet below
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+          }
+        } else if (f1 == at.hi || f1 == end) {
           // the row ends, or the share: the whole row goes to O and LSE, a part of
           // it to the share's partial results, index 1 where the row begins in
           // this share, 0 where it goes on
@@ -467,82 +503,121 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         advance(at);
       }
       cp_async_wait<0>();
+      if (block_row) {
+        // one partial result for the block, in its first share's place (the
+        // others' stay empty): a quarter of what the joining kernel would read
+        const int hk = at.rs / p.head_blocks, hb = at.rs - hk * p.head_blocks;
+        const int hn = min(16, p.group - hb * 16);
+        __syncthreads();
+        float2* stat = reinterpret_cast<float2*>(smem);  // [warp][16], then [warp][16][D] sums
+        float* acc = reinterpret_cast<float*>(smem + kWarps * 16 * sizeof(float2));
+        if (q4 == 0) {
+          stat[warp * 16 + g] = make_float2(m[0], l[0]);
+          stat[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          float* a = acc + (warp * 16 + g) * D + 8 * i + 2 * q4;
+          *reinterpret_cast<float2*>(a) = make_float2(o[i][0], o[i][1]);
+          *reinterpret_cast<float2*>(a + 8 * D) = make_float2(o[i][2], o[i][3]);
+        }
+        __syncthreads();
+        const bool begins = at.lo >= blk0 * W / shares;
+        const bool whole = begins && at.hi == (blk0 + kWarps) * W / shares;
+        for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
+          const int r = x / (D / 8), col = 8 * (x % (D / 8));
+          float mm = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * 16 + r].x);
+          const float ref = mm == -INFINITY ? 0.f : mm;
+          float rs = 0.f, out[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out[e] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 st = stat[w * 16 + r];
+            const float f = fast_exp2(st.x - ref);
+            rs += f * st.y;
+            add_row8(out, f, acc + (w * 16 + r) * D + col);
+          }
+          if (whole) {
+            if (col < p.c.d) write_row(p, b0 + at.j, hk * p.group + hb * 16 + r, col, mm, rs, out);
+            continue;
+          }
+          const long long row = (2 * blk0 + (begins ? 1 : 0)) * 16 + r;
+          float4* a = reinterpret_cast<float4*>(p.part_acc + row * D + col);
+          a[0] = make_float4(out[0], out[1], out[2], out[3]);
+          a[1] = make_float4(out[4], out[5], out[6], out[7]);
+          if (col == 0) {
+            p.part_stat[row] = make_float2(mm, rs);
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w)
+              p.part_stat[2 * (blk0 + w) * 16 + r] = make_float2(-INFINITY, 0.f);
+          }
+        }
+        if (p.batch > kThreads) __syncthreads();
+      }
     }
     chunk_lo = chunk_hi;
     if (p.batch > kThreads) __syncthreads();  // the next chunk overwrites the sequences
   }
 }
 
-// Eight columns of query head h of sequence b: O = out / sum, LSE = ln2 (m + log2 sum).
-__device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, int col, float m, float sum,
-                                          const float (&out)[8]) {
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) =
-      make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
-                 pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
-  if (col == 0)
-    p.lse[static_cast<long long>(b) * p.heads + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-}
-
-// Joins the parts of rows that were cut: a block per (sequence, query head),
-// D / 8 threads over the columns, kJoinThreads / (D / 8) groups over the parts.
-constexpr int kJoinThreads = 256;
+// Joins the parts of rows that were cut: a block per (row, up to 4 of its query
+// heads), D / 8 threads over a head's columns, the others over the parts.
+constexpr int kJoinThreads = 256, kJoinHeads = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
-  constexpr int TPR = D / 8, GROUPS = kJoinThreads / TPR;
-  __shared__ float2 stat[GROUPS];
-  __shared__ float acc[GROUPS][D];
+  constexpr int TPR = D / 8, GROUPS = kJoinThreads / (TPR * kJoinHeads);
+  __shared__ float2 stat[GROUPS][kJoinHeads];
+  __shared__ __align__(16) float acc[GROUPS][kJoinHeads][D];
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
-  const long long before = p.tiles_upto[b], row_tiles = p.tiles_upto[b + 1] - before;
+  const int2 span = p.cut_rows[blockIdx.x];  // first and last share of the row
+  if (span.x >= span.y) return;              // written already
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
-  const long long W = p.tiles_upto[p.batch] * rows_per_seq;
-  const int shares = static_cast<int>(p.tiles_upto[p.batch + 1]);
-  if (row_tiles == 0) return;
-  const int hk = h / p.group, hb = (h - hk * p.group) / 16, r = (h - hk * p.group) % 16;
-  const long long row_lo = before * rows_per_seq + (hk * p.head_blocks + hb) * row_tiles;
-  const int c0 = share_of(row_lo, W, shares), c1 = share_of(row_lo + row_tiles - 1, W, shares);
-  if (c0 == c1) return;  // written already
-  const int group = threadIdx.x / TPR, col = 8 * (threadIdx.x % TPR);
+  const int b = blockIdx.x / rows_per_seq, rs = blockIdx.x - b * rows_per_seq;
+  const int hk = rs / p.head_blocks, hb = rs - hk * p.head_blocks;
+  const int hn = min(16, p.group - hb * 16);
+  const int col = 8 * (threadIdx.x % TPR), x = threadIdx.x / TPR;
+  const int rl = x % kJoinHeads, group = x / kJoinHeads, r = blockIdx.y * kJoinHeads + rl;
   float m = -INFINITY, sum = 0.f, out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.f;
+  if (r < hn) {
 #pragma unroll 4
-  for (int c = c0 + group; c <= c1; c += GROUPS) {
-    const long long part = (2ll * c + (c == c0 ? 1 : 0)) * 16 + r;
-    const float2 st = p.part_stat[part];
-    const float4* a = reinterpret_cast<const float4*>(p.part_acc + part * D + col);
-    const float4 a0 = a[0], a1 = a[1];
-    const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-    const float mm = fmaxf(m, st.x), ref = mm == -INFINITY ? 0.f : mm;
-    const float fo = fast_exp2(m - ref), fn = fast_exp2(st.x - ref);
-    m = mm;
-    sum = sum * fo + st.y * fn;
+    for (int c = span.x + group; c <= span.y; c += GROUPS) {
+      const long long part = (2ll * c + (c == span.x ? 1 : 0)) * 16 + r;
+      const float2 st = p.part_stat[part];
+      if (st.y == 0.f) continue;  // no keys, or in its block's first share
+      const float mm = fmaxf(m, st.x), fo = fast_exp2(m - mm);
+      m = mm;
+      sum = sum * fo + st.y * fast_exp2(st.x - mm);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = out[e] * fo + v[e] * fn;
+      for (int e = 0; e < 8; ++e) out[e] *= fo;
+      add_row8(out, fast_exp2(st.x - mm), p.part_acc + part * D + col);
+    }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[group][col + e] = out[e];
-  if (col == 0) stat[group] = make_float2(m, sum);
+  for (int e = 0; e < 8; ++e) acc[group][rl][col + e] = out[e];
+  if (col == 0) stat[group][rl] = make_float2(m, sum);
   __syncthreads();
-  if (group != 0 || col >= p.c.d) return;
-  float mm = -INFINITY;
+  if (group != 0 || col >= p.c.d || r >= hn) return;
+  m = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < GROUPS; ++w) mm = fmaxf(mm, stat[w].x);
-  const float ref = mm == -INFINITY ? 0.f : mm;
+  for (int w = 0; w < GROUPS; ++w) m = fmaxf(m, stat[w][rl].x);
+  const float ref = m == -INFINITY ? 0.f : m;
   sum = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.f;
 #pragma unroll
   for (int w = 0; w < GROUPS; ++w) {
-    const float f = fast_exp2(stat[w].x - ref);
-    sum += f * stat[w].y;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = fmaf(f, acc[w][col + e], out[e]);
+    const float f = fast_exp2(stat[w][rl].x - ref);
+    sum += f * stat[w][rl].y;
+    add_row8(out, f, &acc[w][rl][col]);
   }
-  write_row(p, b, h, col, mm, sum, out);
+  write_row(p, b, hk * p.group + hb * 16 + r, col, m, sum, out);
 }
 
 // Grid and workspace of a call, from what the host knows: the longest that a
@@ -567,7 +642,7 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const long long blocks = (rows * tiles + kMinShare - 1) / kMinShare;  // one warp each
   p.grid = blocks < 148ll * per_sm ? blocks : 148ll * per_sm;
   p.cut = tiles > 1;
-  p.off_stat = ((static_cast<size_t>(batch) + 2) * 8 + 255) / 256 * 256;
+  p.off_stat = (static_cast<size_t>(rows) * sizeof(int2) + 255) / 256 * 256;
   const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
   p.off_acc = p.off_stat + parts * sizeof(float2);
   p.bytes = p.cut ? p.off_acc + parts * D * sizeof(float) : 0;
@@ -577,6 +652,7 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
 template <int D>
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t stream) {
   using C = DecodeCfg<D>;
+  static_assert(kWarps * 16 * (8 + D * 4) <= C::OFF_VALID, "a block's parts fit the ring");
   auto kern = attend_kernel<D>;
   static OncePerContext prepared;
   const cudaError_t e = prepared.run([&]() -> cudaError_t {
@@ -588,14 +664,16 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
   AttendParams a = p;
   if (plan.cut) {
     char* ws = static_cast<char*>(workspace);
-    a.tiles_upto = reinterpret_cast<long long*>(ws);
+    a.cut_rows = reinterpret_cast<int2*>(ws);
     a.part_stat = reinterpret_cast<float2*>(ws + plan.off_stat);
     a.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
   }
   cudaError_t r = launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), dim3(kThreads), C::SMEM,
                                     stream, a);
   if (r == cudaSuccess && plan.cut)
-    r = launch_overlapped(join_kernel<D>, dim3(static_cast<unsigned>(p.batch * p.heads)),
+    r = launch_overlapped(join_kernel<D>,
+                          dim3(static_cast<unsigned>(p.batch * p.c.heads_kv * p.head_blocks),
+                               static_cast<unsigned>(((p.group < 16 ? p.group : 16) + kJoinHeads - 1) / kJoinHeads)),
                           dim3(kJoinThreads), 0, stream, a);
   return r;
 }
@@ -653,7 +731,7 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * fa::kLog2e);
   p.window = window;
   p.sinks = sinks;
-  p.tiles_upto = nullptr;
+  p.cut_rows = nullptr;
   p.part_stat = nullptr;
   p.part_acc = nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
