@@ -88,6 +88,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Asks for a line that will be read soon.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 constexpr int kWarps = 4;
 
 template <int D>
@@ -98,7 +103,10 @@ struct DecodeCfg {
   static constexpr uint32_t STAGE = 2 * KT * ROW;  // K then V
   static constexpr uint32_t WARP = STAGES * STAGE;
   static constexpr uint32_t OFF_VALID = kWarps * WARP;  // [warp][stage] key bits
-  static constexpr uint32_t SMEM = OFF_VALID + kWarps * STAGES * 4;
+  // Q: registers, but at D = 256, where O fills them, a tile of 16 rows per warp
+  static constexpr bool Q_SMEM = D == 256;
+  static constexpr uint32_t OFF_Q = (OFF_VALID + kWarps * STAGES * 4 + 127) / 128 * 128;
+  static constexpr uint32_t SMEM = OFF_Q + (Q_SMEM ? kWarps * 16 * ROW : 0);
   static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
 };
 
@@ -107,10 +115,17 @@ constexpr int kThreads = kWarps * 32;
 // cost more in joining than they save.
 constexpr int kMinShare = 4;
 
-// The share that holds tile f: shares are [c W / n, (c + 1) W / n).
-__device__ __forceinline__ int share_of(long long f, long long W, int n) {
-  return static_cast<int>(((f + 1) * n - 1) / W);
-}
+// W tiles in n shares: the first W % n hold one tile more.  All tile counts
+// fit 32 bits (checked on the host: 64-bit divisions took 1 us of every call).
+struct Shares {
+  uint32_t n, each, more;
+  __device__ __forceinline__ Shares(uint32_t W, uint32_t count) : n(count), each(W / count), more(W % count) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ uint32_t holding(uint32_t f) const {
+    const uint32_t big = more * (each + 1);
+    return f < big ? f / (each + 1) : more + (f - big) / each;
+  }
+};
 
 // Keys a query sees: u -> key position (see the head of the file).
 struct Visible {
@@ -148,15 +163,15 @@ __device__ __forceinline__ void add_row8(float (&out)[8], float f, const float* 
 // The sequences that a block looks at together, in shared memory.
 struct Seqs {
   int len[kThreads], tiles[kThreads], slot[kThreads];
-  long long upto[kThreads];  // running sum of tiles
-  long long scan[kWarps];
+  uint32_t upto[kThreads];  // running sum of tiles
+  uint32_t scan[kWarps];
 };
 
 // A place in the walk: tile f of the row that spans [lo, hi) of the batch's
-// tiles, row rs (K / V head, block of heads) of sequence j of the chunk.
+// tiles, row rs (K / V head hk, block of heads) of sequence j of the chunk.
 struct Cursor {
-  long long f, lo, hi;
-  int j, rs;
+  uint32_t f, lo, hi;
+  int j, rs, hk;
 };
 
 template <int D>
@@ -165,9 +180,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
   constexpr int KT = C::KT, STAGES = C::STAGES;
   griddep_wait();
   griddep_launch_dependents();
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Seqs sq;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, q4 = lane & 3;  // row and column group of the matrix fragments
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
 
@@ -186,17 +202,17 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
     return tiles;
   };
   // inclusive prefix sum over the block into sq.upto; returns the sum of all
-  auto scan = [&](long long x) -> long long {
+  auto scan = [&](uint32_t x) -> uint32_t {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, off);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += y;
     }
     if (lane == 31) sq.scan[warp] = x;
     __syncthreads();
-    long long before = 0, all = 0;
+    uint32_t before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (uint32_t w = 0; w < kWarps; ++w) {
       if (w < warp) before += sq.scan[w];
       all += sq.scan[w];
     }
@@ -204,26 +220,27 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
     __syncthreads();
     return all;
   };
-  long long sum = 0, part = 0;  // tiles of one row per sequence
+  uint32_t sum = 0, part = 0;  // tiles of one row per sequence
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     part = scan(load_seq(b0 + threadIdx.x));
     sum += part;
   }
-  const long long W = sum * rows_per_seq;
-  const long long want = (W + kMinShare - 1) / kMinShare;
-  const long long most = static_cast<long long>(gridDim.x) * kWarps;
-  const int shares = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+  const uint32_t W = sum * rows_per_seq;
+  const uint32_t grid = gridDim.x, want = W / kMinShare + (W % kMinShare != 0);
+  const Shares sh(W, min(max(want, 1u), grid * kWarps));
   // few shares: one or two warps of a block, so that they spread over the SMs
-  const int active = shares <= static_cast<int>(gridDim.x) ? 1 : shares <= 2 * static_cast<int>(gridDim.x) ? 2 : kWarps;
-  const long long blk0 = static_cast<long long>(blockIdx.x) * kWarps;
-  const int share = warp < active ? blockIdx.x * active + warp : shares;
-  const long long lo = share < shares ? share * W / shares : W;
-  const long long hi = share < shares ? (share + 1) * W / shares : W;
+  const uint32_t active = sh.n <= grid ? 1 : sh.n <= 2 * grid ? 2 : kWarps;
+  const uint32_t blk0 = blockIdx.x * active;
+  const uint32_t share = warp < active ? blk0 + warp : sh.n;
+  const uint32_t lo = share < sh.n ? sh.begin(share) : W, hi = share < sh.n ? sh.begin(share + 1) : W;
+  // the block's own range, where all its warps have a share
+  const bool full = active == kWarps && blk0 + kWarps <= sh.n;
+  const uint32_t blk_lo = full ? sh.begin(blk0) : 0, blk_hi = full ? sh.begin(blk0 + kWarps) : 0;
 
   const uint32_t ring = smem_u32(smem) + warp * C::WARP;
   uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
 
-  long long chunk_lo = 0;  // tile at which this chunk of sequences begins
+  uint32_t chunk_lo = 0;  // tile at which this chunk of sequences begins
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     if (p.batch > kThreads) part = scan(load_seq(b0 + threadIdx.x));  // else it is still there
     // rows without keys belong to no share: the last block writes them
@@ -241,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
             p.cut_rows[static_cast<long long>(b) * rows_per_seq + x] = make_int2(0, 0);
       }
     }
-    const long long chunk_hi = chunk_lo + part * rows_per_seq;
-    const long long from = lo > chunk_lo ? lo : chunk_lo, end = hi < chunk_hi ? hi : chunk_hi;
+    const uint32_t chunk_hi = chunk_lo + part * rows_per_seq;
+    const uint32_t from = max(lo, chunk_lo), end = min(hi, chunk_hi);
     if (from < end) {
       // the row of tile `from`: the first sequence whose running sum passes it
       Cursor at;
       {
-        const long long fs = (from - chunk_lo) / rows_per_seq;
+        const uint32_t fs = (from - chunk_lo) / rows_per_seq;
         int a = 0, z = kThreads - 1;
         while (a < z) {
           const int mid = (a + z) / 2;
@@ -255,10 +272,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           else a = mid + 1;
         }
         at.j = a;
-        const int tiles = sq.tiles[a];
-        const long long seq_lo = chunk_lo + (sq.upto[a] - tiles) * rows_per_seq;
-        at.rs = static_cast<int>((from - seq_lo) / tiles);
-        at.lo = seq_lo + static_cast<long long>(at.rs) * tiles;
+        const uint32_t tiles = sq.tiles[a];
+        const uint32_t seq_lo = chunk_lo + (sq.upto[a] - tiles) * rows_per_seq;
+        at.rs = (from - seq_lo) / tiles;
+        at.hk = at.rs / p.head_blocks;
+        at.lo = seq_lo + at.rs * tiles;
         at.hi = at.lo + tiles;
         at.f = from;
       }
@@ -269,23 +287,30 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           do ++c.j;
           while (sq.tiles[c.j] == 0);
         }
+        c.hk = p.head_blocks == 1 ? c.rs : c.rs / p.head_blocks;
         c.lo = c.hi;
         c.hi += sq.tiles[c.j];
       };
 
       // Page and row of this lane's key (lane & (KT - 1)) of the cursor's tile,
       // and the tile's K / V head.  The table cell is asked for a round before
-      // the copies need it, and nothing is computed from it until then: used at
-      // once, every round waits for the load (0.3 us).
+      // copies need it, and nothing is computed from it until then.
       struct Key {
         int page, row, hk;
       };
       auto locate = [&](const Cursor& c) -> Key {
-        Key r{-1, 0, 0};
+        Key r{-1, 0, c.hk};
         if (c.f >= end) return r;
+        if (c.f == c.lo || c.f == from) {
+          // a row begins: its Q into L2, a 128-byte line a lane
+          const int hb = c.rs - c.hk * p.head_blocks, lines = (2 * p.c.d + 127) / 128;
+          const int h = lane / lines;
+          if (h < min(16, p.group - hb * 16))
+            prefetch_l2(p.q + (b0 + c.j) * p.q_batch + (c.hk * p.group + hb * 16 + h) * p.q_head +
+                        (lane - h * lines) * 64);
+        }
         const Visible vis = visible_of(sq.len[c.j], p.window, p.sinks);
         const int u = static_cast<int>(c.f - c.lo) * KT + (lane & (KT - 1));
-        r.hk = c.rs / p.head_blocks;
         if (u < vis.count) {
           const int j = vis.key(u);
           const int cell = j / p.c.page_size;
@@ -299,21 +324,34 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         constexpr int CH = D / 8, RPI = 32 / CH;  // pieces of a row, rows per step
         const int c = lane % CH;
         const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
-        const bool has = r.page >= 0 && r.page < p.c.pages;
-        const long long k0 = r.page * p.c.k_page + r.hk * p.c.k_head + r.row * p.c.k_row;
-        const long long v0 = r.page * p.c.v_page + r.hk * p.c.v_head + r.row * p.c.v_row;
-        const uint32_t live = __ballot_sync(0xffffffffu, has);
+        const uint32_t live = __ballot_sync(0xffffffffu, r.page >= 0 && r.page < p.c.pages);
         if (lane == 0) valid[stage] = live;
         const bool col_ok = 8 * c < p.c.d;
+        const __nv_bfloat16* kh = p.k + r.hk * p.c.k_head + 8 * c;
+        const __nv_bfloat16* vh = p.v + r.hk * p.c.v_head + 8 * c;
+        const int page0 = __shfl_sync(0xffffffffu, r.page, 0), row0 = __shfl_sync(0xffffffffu, r.row, 0);
+        if (__all_sync(0xffffffffu, r.page == page0 && r.row == row0 + (lane & (KT - 1)) && col_ok) &&
+            (live & 1u)) {
+          // consecutive rows of one page
+          const __nv_bfloat16* kp = kh + page0 * p.c.k_page + (row0 + lane / CH) * p.c.k_row;
+          const __nv_bfloat16* vp = vh + page0 * p.c.v_page + (row0 + lane / CH) * p.c.v_row;
 #pragma unroll
-        for (int s = 0; s < KT / RPI; ++s) {
-          const int row = s * RPI + lane / CH;
-          const long long ko = __shfl_sync(0xffffffffu, k0, row);
-          const long long vo = __shfl_sync(0xffffffffu, v0, row);
-          const bool ok = col_ok && ((live >> row) & 1u);
-          const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
-          cp_async16(kdst + dst, p.k + (ok ? ko + 8 * c : 0), ok);
-          cp_async16(vdst + dst, p.v + (ok ? vo + 8 * c : 0), ok);
+          for (int s = 0; s < KT / RPI; ++s) {
+            const int row = s * RPI + lane / CH;
+            const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+            cp_async16(kdst + dst, kp + s * RPI * p.c.k_row, true);
+            cp_async16(vdst + dst, vp + s * RPI * p.c.v_row, true);
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < KT / RPI; ++s) {
+            const int row = s * RPI + lane / CH;
+            const int page = __shfl_sync(0xffffffffu, r.page, row), at_row = __shfl_sync(0xffffffffu, r.row, row);
+            const bool ok = col_ok && ((live >> row) & 1u);
+            const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+            cp_async16(kdst + dst, ok ? kh + page * p.c.k_page + at_row * p.c.k_row : p.k, ok);
+            cp_async16(vdst + dst, ok ? vh + page * p.c.v_page + at_row * p.c.v_row : p.v, ok);
+          }
         }
       };
 
@@ -334,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
       Key next = locate(fill);
 
       // whether the block's four shares lie in one row
-      const bool block_row = active == kWarps && shares >= blk0 + kWarps && at.lo <= blk0 * W / shares &&
-                             at.hi >= (blk0 + kWarps) * W / shares;
-      uint32_t qa[D / 16][4];     // Q as the A operand: rows g and g + 8
+      const bool block_row = full && at.lo <= blk_lo && at.hi >= blk_hi;
+      uint32_t qa[C::Q_SMEM ? 1 : D / 16][4];  // Q as the A operand: rows g and g + 8
+      const uint32_t qs = smem_u32(smem) + C::OFF_Q + warp * 16 * C::ROW;
       float o[D / 8][4];
       float m[2], l[2];           // rows g, g + 8; l: this lane's part
       bool begin = true;
@@ -348,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         cp_async_commit();
         advance(fill);
         next = locate(fill);
-        const int hk = at.rs / p.head_blocks, hb = at.rs - hk * p.head_blocks;
+        const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
         const int h0 = hk * p.group + hb * 16;      // first query head of the row
         const int hn = min(16, p.group - hb * 16);  // its query heads
         const int b = b0 + at.j;
@@ -356,18 +394,28 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           // the joining kernel learns the row's shares from the one it begins in
           if (p.cut_rows != nullptr && at.lo >= lo && lane == 0)
             p.cut_rows[static_cast<long long>(b) * rows_per_seq + at.rs] =
-                make_int2(share, at.hi <= hi ? share : share_of(at.hi - 1, W, shares));
+                make_int2(share, at.hi <= hi ? share : sh.holding(at.hi - 1));
           // Q: zero past the row's heads and past d
           const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
+          if constexpr (C::Q_SMEM) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int r = g + 8 * (u & 1), col = 16 * kk + 8 * (u >> 1) + 2 * q4;
-              qa[kk][u] = r < hn && col < p.c.d
-                              ? *reinterpret_cast<const uint32_t*>(q0 + r * p.q_head + col)
-                              : 0u;
+            for (int x = lane; x < 16 * (D / 8); x += 32) {
+              const int r = x / (D / 8), c = x % (D / 8);
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (r < hn && 8 * c < p.c.d) v = *reinterpret_cast<const uint4*>(q0 + r * p.q_head + 8 * c);
+              st_shared_v4(qs + r * C::ROW + ((c ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
             }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int r = g + 8 * (u & 1), col = 16 * kk + 8 * (u >> 1) + 2 * q4;
+                qa[kk][u] = r < hn && col < p.c.d
+                                ? *reinterpret_cast<const uint32_t*>(q0 + r * p.q_head + col)
+                                : 0u;
+              }
+          }
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -387,16 +435,20 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
 #pragma unroll
           for (int u = 0; u < 4; ++u) s[i][u] = s1[i][u] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if constexpr (C::Q_SMEM)
+            ldsm_x4(qs + (lane & 15) * C::ROW + (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4), qa[0]);
+          const uint32_t(&qk)[4] = qa[C::Q_SMEM ? 0 : kk];
 #pragma unroll
           for (int kt = 0; kt < KT / 16; ++kt) {
             uint32_t kb[4];
             const int row = kt * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
             const int ch = 2 * kk + ((lane >> 3) & 1);
             ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), kb);
-            mma16816(kk & 1 ? s1[2 * kt] : s[2 * kt], qa[kk], kb[0], kb[1]);
-            mma16816(kk & 1 ? s1[2 * kt + 1] : s[2 * kt + 1], qa[kk], kb[2], kb[3]);
+            mma16816(kk & 1 ? s1[2 * kt] : s[2 * kt], qk, kb[0], kb[1]);
+            mma16816(kk & 1 ? s1[2 * kt + 1] : s[2 * kt + 1], qk, kb[2], kb[3]);
           }
+        }
 #pragma unroll
         for (int i = 0; i < KT / 8; ++i)
 #pragma unroll
@@ -460,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         }
         stage = stage + 1 == STAGES ? 0 : stage + 1;
 
-        const long long f1 = at.f + 1;
+        const uint32_t f1 = at.f + 1;
         if (block_row && f1 == end) {
           // all of the block's shares are parts of this row: they meet below
 #pragma unroll
@@ -506,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
       if (block_row) {
         // one partial result for the block, in its first share's place (the
         // others' stay empty): a quarter of what the joining kernel would read
-        const int hk = at.rs / p.head_blocks, hb = at.rs - hk * p.head_blocks;
+        const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
         const int hn = min(16, p.group - hb * 16);
         __syncthreads();
         float2* stat = reinterpret_cast<float2*>(smem);  // [warp][16], then [warp][16][D] sums
@@ -522,8 +574,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           *reinterpret_cast<float2*>(a + 8 * D) = make_float2(o[i][2], o[i][3]);
         }
         __syncthreads();
-        const bool begins = at.lo >= blk0 * W / shares;
-        const bool whole = begins && at.hi == (blk0 + kWarps) * W / shares;
+        const bool begins = at.lo >= blk_lo, whole = begins && at.hi == blk_hi;
         for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
           const int r = x / (D / 8), col = 8 * (x % (D / 8));
           float mm = -INFINITY;
@@ -544,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
             if (col < p.c.d) write_row(p, b0 + at.j, hk * p.group + hb * 16 + r, col, mm, rs, out);
             continue;
           }
-          const long long row = (2 * blk0 + (begins ? 1 : 0)) * 16 + r;
+          const long long row = (2ll * blk0 + (begins ? 1 : 0)) * 16 + r;
           float4* a = reinterpret_cast<float4*>(p.part_acc + row * D + col);
           a[0] = make_float4(out[0], out[1], out[2], out[3]);
           a[1] = make_float4(out[4], out[5], out[6], out[7]);
@@ -552,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
             p.part_stat[row] = make_float2(mm, rs);
 #pragma unroll
             for (int w = 1; w < kWarps; ++w)
-              p.part_stat[2 * (blk0 + w) * 16 + r] = make_float2(-INFINITY, 0.f);
+              p.part_stat[2ll * (blk0 + w) * 16 + r] = make_float2(-INFINITY, 0.f);
           }
         }
         if (p.batch > kThreads) __syncthreads();
@@ -625,6 +676,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
 // batch cannot have a share for one warp of each; no row can be cut, and none
 // has to be joined, where none can have more than one tile.
 struct Plan {
+  long long tiles;  // at most, of the whole batch
   long long grid;
   bool cut;
   size_t off_stat, off_acc, bytes;
@@ -639,6 +691,7 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const long long tiles = (most + KT - 1) / KT;
   const long long rows = static_cast<long long>(batch) * c.heads_kv * ((heads / c.heads_kv + 15) / 16);
   Plan p;
+  p.tiles = rows * tiles;
   const long long blocks = (rows * tiles + kMinShare - 1) / kMinShare;  // one warp each
   p.grid = blocks < 148ll * per_sm ? blocks : 148ll * per_sm;
   p.cut = tiles > 1;
@@ -712,7 +765,9 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   if (!fa::cache_aligned(q, 16) || !fa::cache_aligned(o, 16) || !fa::cache_aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(batch) * heads > 0x7FFFFFFF) return FA_ERR_UNSUPPORTED;
-  const size_t need = fa::plan_of(p.c, batch, heads, window, sinks).bytes;
+  const fa::Plan plan = fa::plan_of(p.c, batch, heads, window, sinks);
+  if (plan.tiles > 0xFFFFFFFFll - 65536) return FA_ERR_UNSUPPORTED;  // 32-bit counts in the kernels
+  const size_t need = plan.bytes;
   if (need > 0 && (!fa::cache_aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_WORKSPACE;
   p.k = static_cast<const __nv_bfloat16*>(p.c.k) + layer * p.c.k_layer;
   p.v = static_cast<const __nv_bfloat16*>(p.c.v) + layer * p.c.v_layer;
