@@ -111,10 +111,6 @@ struct DecodeCfg {
 };
 
 constexpr int kThreads = kWarps * 32;
-// A share is at least this many tiles (of the whole batch's): smaller ones
-// cost more in joining than they save.
-constexpr int kMinShare = 4;
-
 // W tiles in n shares: the first W % n hold one tile more.  All tile counts
 // fit 32 bits (checked on the host: 64-bit divisions took 1 us of every call).
 struct Shares {
@@ -226,8 +222,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
     sum += part;
   }
   const uint32_t W = sum * rows_per_seq;
-  const uint32_t grid = gridDim.x, want = W / kMinShare + (W % kMinShare != 0);
-  const Shares sh(W, min(max(want, 1u), grid * kWarps));
+  // (down to one tile each: shares of at least four took 10.8 us for one
+  // sequence of 500 keys where these take 8.7, joining included)
+  const uint32_t grid = gridDim.x;
+  const Shares sh(W, min(max(W, 1u), grid * kWarps));
   // few shares: one or two warps of a block, so that they spread over the SMs
   const uint32_t active = sh.n <= grid ? 1 : sh.n <= 2 * grid ? 2 : kWarps;
   const uint32_t blk0 = blockIdx.x * active;
@@ -615,66 +613,95 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
 }
 
 // Joins the parts of rows that were cut: a block per (row, up to 4 of its query
-// heads), D / 8 threads over a head's columns, the others over the parts.
+// heads).  First every part's weight 2^(m - M), all statistics at once, then
+// the weighted sums: D / 8 threads over a head's columns, the others over the
+// parts, whose loads wait for nothing (with the maximum carried from part to
+// part, 16 rows of 37 parts at d = 256 took 13 us).
 constexpr int kJoinThreads = 256, kJoinHeads = 4;
+constexpr int kJoinParts = 148 * 2 * kWarps;  // a row has no more shares than a grid has warps
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
   constexpr int TPR = D / 8, GROUPS = kJoinThreads / (TPR * kJoinHeads);
-  __shared__ float2 stat[GROUPS][kJoinHeads];
+  __shared__ float weight[kJoinHeads][kJoinParts];
+  __shared__ float2 red[kJoinThreads / 32][kJoinHeads];
   __shared__ __align__(16) float acc[GROUPS][kJoinHeads][D];
   griddep_wait();
   griddep_launch_dependents();
   const int2 span = p.cut_rows[blockIdx.x];  // first and last share of the row
   if (span.x >= span.y) return;              // written already
+  const int parts = span.y - span.x + 1;
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
   const int b = blockIdx.x / rows_per_seq, rs = blockIdx.x - b * rows_per_seq;
   const int hk = rs / p.head_blocks, hb = rs - hk * p.head_blocks;
-  const int hn = min(16, p.group - hb * 16);
+  const int hn = min(16, p.group - hb * 16) - blockIdx.y * kJoinHeads;  // this block's heads, and more
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // partial result i of head r of this block (see attend_kernel)
+  auto row_of = [&](int i, int r) {
+    return (2ll * (span.x + i) + (i == 0 ? 1 : 0)) * 16 + blockIdx.y * kJoinHeads + r;
+  };
+
+  // weights: thread = (head threadIdx.x % 4, parts threadIdx.x / 4, + 64, ...);
+  // a part without keys, or merged into its block's first share, has sum 0
+  const int hr = threadIdx.x % kJoinHeads;
+  float m = -INFINITY;
+  for (int i = threadIdx.x / kJoinHeads; i < parts; i += kJoinThreads / kJoinHeads) {
+    float x = -INFINITY;
+    if (hr < hn) {
+      const float2 st = p.part_stat[row_of(i, hr)];
+      if (st.y > 0.f) x = st.x;
+    }
+    weight[hr][i] = x;
+    m = fmaxf(m, x);
+  }
+#pragma unroll
+  for (int o = kJoinHeads; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane < kJoinHeads) red[warp][lane].x = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w][hr].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  for (int i = threadIdx.x / kJoinHeads; i < parts; i += kJoinThreads / kJoinHeads) {
+    const float f = fast_exp2(weight[hr][i] - ref);
+    weight[hr][i] = f;
+    if (f > 0.f) sum += f * p.part_stat[row_of(i, hr)].y;
+  }
+  // (a fixed order of sums: lanes, then warps, then threads of a head below)
+#pragma unroll
+  for (int o = kJoinHeads; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane < kJoinHeads) red[warp][lane].y = sum;
+  __syncthreads();
+
   const int col = 8 * (threadIdx.x % TPR), x = threadIdx.x / TPR;
-  const int rl = x % kJoinHeads, group = x / kJoinHeads, r = blockIdx.y * kJoinHeads + rl;
-  float m = -INFINITY, sum = 0.f, out[8];
+  const int r = x % kJoinHeads, group = x / kJoinHeads;
+  float out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.f;
   if (r < hn) {
-#pragma unroll 4
-    for (int c = span.x + group; c <= span.y; c += GROUPS) {
-      const long long part = (2ll * c + (c == span.x ? 1 : 0)) * 16 + r;
-      const float2 st = p.part_stat[part];
-      if (st.y == 0.f) continue;  // no keys, or in its block's first share
-      const float mm = fmaxf(m, st.x), fo = fast_exp2(m - mm);
-      m = mm;
-      sum = sum * fo + st.y * fast_exp2(st.x - mm);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] *= fo;
-      add_row8(out, fast_exp2(st.x - mm), p.part_acc + part * D + col);
-    }
+#pragma unroll 8
+    for (int i = group; i < parts; i += GROUPS)
+      if (weight[r][i] > 0.f) add_row8(out, weight[r][i], p.part_acc + row_of(i, r) * D + col);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[group][rl][col + e] = out[e];
-  if (col == 0) stat[group][rl] = make_float2(m, sum);
+  for (int e = 0; e < 8; ++e) acc[group][r][col + e] = out[e];
   __syncthreads();
   if (group != 0 || col >= p.c.d || r >= hn) return;
-  m = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < GROUPS; ++w) m = fmaxf(m, stat[w][rl].x);
-  const float ref = m == -INFINITY ? 0.f : m;
-  sum = 0.f;
+  for (int w = 1; w < GROUPS; ++w) add_row8(out, 1.f, &acc[w][r][col]);
+  float mm = -INFINITY, all = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] = 0.f;
-#pragma unroll
-  for (int w = 0; w < GROUPS; ++w) {
-    const float f = fast_exp2(stat[w][rl].x - ref);
-    sum += f * stat[w][rl].y;
-    add_row8(out, f, &acc[w][rl][col]);
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    mm = fmaxf(mm, red[w][r].x);
+    all += red[w][r].y;
   }
-  write_row(p, b, hk * p.group + hb * 16 + r, col, m, sum, out);
+  write_row(p, b, hk * p.group + hb * 16 + blockIdx.y * kJoinHeads + r, col, mm, all, out);
 }
 
 // Grid and workspace of a call, from what the host knows: the longest that a
 // sequence may see.  One block per resident slot of the GPU, fewer where the
-// batch cannot have a share for one warp of each; no row can be cut, and none
-// has to be joined, where none can have more than one tile.
+// batch cannot have as many tiles; no row can be cut, and none has to be
+// joined, where none can have more than one tile.
 struct Plan {
   long long tiles;  // at most, of the whole batch
   long long grid;
@@ -692,8 +719,7 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const long long rows = static_cast<long long>(batch) * c.heads_kv * ((heads / c.heads_kv + 15) / 16);
   Plan p;
   p.tiles = rows * tiles;
-  const long long blocks = (rows * tiles + kMinShare - 1) / kMinShare;  // one warp each
-  p.grid = blocks < 148ll * per_sm ? blocks : 148ll * per_sm;
+  p.grid = p.tiles < 148ll * per_sm ? p.tiles : 148ll * per_sm;
   p.cut = tiles > 1;
   p.off_stat = (static_cast<size_t>(rows) * sizeof(int2) + 255) / 256 * 256;
   const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
