@@ -249,7 +249,9 @@ fa_status_t fa_fwd_ex(const fa_attention_desc_t* desc, const void* q, const void
  * 256); with grouped K / V heads whose backward units are split into S parts
  * (few units for the SM count), two fp32 dK / dV areas of
  * S * tb * heads_kv * key rows * D elements more (tb = B padded, 1 packed; key
- * rows = seqlen_k padded, total_k packed).  0 if the description is invalid. */
+ * rows = seqlen_k padded, total_k packed); with a window and first tokens, two
+ * fp32 areas of the first tokens' partial dK / dV more, at most 1184 * 128 * D
+ * elements each.  0 if the description is invalid. */
 size_t fa_bwd_ex_workspace_size(const fa_attention_desc_t* desc);
 
 /* Backward pass for a general layout (dQ like Q, dK / dV like K / V; the

@@ -294,11 +294,41 @@ int64_t kv_acc_elems(const Problem& p) {
   return static_cast<int64_t>(s) * p.tb() * p.Hkv * p.rows_k() * p.D;
 }
 
+// First keys under a sliding window, in the backward: see BwdParams.  A unit of
+// a first key tile walks all later query tiles where the others walk the
+// window, so its walk is cut into pieces of at least a window's length (and 8
+// tiles), fewer where the first tiles' units alone would fill the GPU four
+// times.  (16K sequence, 4 K / V heads of 4 query heads, d = 128, window 1024, 4
+// first keys: 1430 us with whole walks, 627 without first keys.)
+struct SinkCut {
+  int tiles = 0, chunks = 0, len = 0;
+  int64_t elems = 0;  // of each of the dK / dV slices
+};
+
+SinkCut sink_cut_of(const Problem& p) {
+  SinkCut c;
+  if (p.window == 0 || p.sinks == 0) return c;
+  const int64_t key_tiles = (p.nk + 127) / 128, q_tiles = (p.nq + 127) / 128;
+  const int64_t tiles = (p.sinks + 127) / 128 < key_tiles ? (p.sinks + 127) / 128 : key_tiles;
+  const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * split_of(p) * tiles;
+  if (units >= 4 * 148) return c;
+  int64_t len = p.window / 128 + 1;
+  if (len < 8) len = 8;
+  if (len < (q_tiles * units + 4 * 148 - 1) / (4 * 148)) len = (q_tiles * units + 4 * 148 - 1) / (4 * 148);
+  if (q_tiles <= len) return c;
+  c.tiles = static_cast<int>(tiles);
+  c.len = static_cast<int>(len);
+  c.chunks = static_cast<int>((q_tiles + len - 1) / len);
+  c.elems = (1 + c.chunks) * units * 128 * p.D;
+  return c;
+}
+
 size_t workspace_bytes_of(const Problem& p) {
   int npad = 0;
   int64_t rtot = 0;
   const uint64_t rows = static_cast<uint64_t>(ws_rows(p, &npad, &rtot));
-  const uint64_t bytes = rows * (4ull + 4ull + 4ull * p.D) + 8ull * kv_acc_elems(p);
+  const uint64_t bytes = rows * (4ull + 4ull + 4ull * p.D) + 8ull * kv_acc_elems(p) +
+                         8ull * sink_cut_of(p).elems;
   return static_cast<size_t>((bytes + 255) / 256 * 256);
 }
 
@@ -324,6 +354,7 @@ void set_extents(const Problem& pr, int* status, fa::Extents* e, fa::Rows* rows)
                 : 0;
   e->seqlens = pr.seqlens != nullptr ? pr.B : 0;
   e->kvacc = kv_acc_elems(pr);
+  e->sink = sink_cut_of(pr).elems;
   rows->n_cu = pr.packed ? pr.B + 1 : 0;
   rows->status = status;
 }
@@ -398,6 +429,13 @@ fa_status_t bwd_params(fa::BwdParams* p, const Problem& pr, const void* workspac
   p->rows_tb = pr.tb();
   p->ws_dk = p->split > 1 ? p->ws_dq + rows * pr.D : nullptr;
   p->ws_dv = p->split > 1 ? p->ws_dk + kv_acc_elems(pr) : nullptr;
+  const SinkCut cut = sink_cut_of(pr);
+  p->sink_tiles = cut.tiles;
+  p->sink_chunks = cut.chunks;
+  p->sink_len = cut.len;
+  p->sink_units = static_cast<long long>(pr.B) * pr.Hkv * p->split * cut.tiles * cut.chunks;
+  p->ws_sk = cut.tiles > 0 ? p->ws_dq + rows * pr.D + 2 * kv_acc_elems(pr) : nullptr;
+  p->ws_sv = cut.tiles > 0 ? p->ws_sk + cut.elems : nullptr;
   p->Npad = npad;
   p->Rtot = rtot;
   lse_strides(pr, &p->lse_sb, &p->lse_sh);
@@ -485,6 +523,7 @@ fa_status_t run_bwd(const Problem& pr, const void* q, const void* k, const void*
     return FA_ERR_CUDA;
   if (fa::launch_bwd_post(pr.D, p, s) != cudaSuccess) return FA_ERR_CUDA;
   if (p.split > 1 && fa::launch_bwd_kv_post(pr.D, p, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (p.sink_tiles > 0 && fa::launch_bwd_sink_post(pr.D, p, s) != cudaSuccess) return FA_ERR_CUDA;
   return FA_OK;
 }
 

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(256) bwd_kv_post_kernel(const BwdParams p) {
   const Seq sq = seq_of(p.rows, b);
   const int j = blockIdx.x * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
   const int part = static_cast<int>(threadIdx.x) % G;
-  if (j >= sq.lk || part * 8 >= p.d_real) return;
+  if (j >= sq.lk || part * 8 >= p.d_real || j < 128 * p.sink_tiles) return;
   const long long rows_k = p.rows.cu_k == nullptr ? p.rows.nk : p.rows.total_k;
   const long long kr = static_cast<long long>(sq.k0) + j;
   const long long acc = ((static_cast<long long>(sq.tb) * n_kv + hk) * rows_k + kr) * D + part * 8;
@@ -351,6 +351,58 @@ __global__ void __launch_bounds__(256) bwd_kv_post_kernel(const BwdParams p) {
   cvt(p.ws_dv + acc, static_cast<__nv_bfloat16*>(p.dv) + dv_off);
 }
 
+// The query tiles past the window of key tile kb of a sequence (lq queries, off =
+// keys - queries): from the later of the tile's first query tile and the end of
+// its last key's window.
+__device__ __forceinline__ int sink_from(int kb, int window, int off, int nqb) {
+  const int lo = kb * 128 - off, last = kb * 128 + 127 + window - 1 - off;
+  return max(lo <= 0 ? 0 : lo / 128, last < 0 ? 0 : min(nqb, last / 128 + 1));
+}
+
+// dK, dV of the first key tiles = bf16(sum over the slices of their units, the
+// ordinary one first, then the walk's pieces in order): grid (row blocks of
+// those tiles) x (B * H_kv).  The slices hold scaled gradients.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_post_kernel(const BwdParams p) {
+  constexpr int G = D / 8;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n_kv = p.H / p.group;
+  const int bh = blockIdx.y;
+  const int b = bh / n_kv, hk = bh % n_kv;
+  const Seq sq = seq_of(p.rows, b);
+  const int j = blockIdx.x * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
+  const int part = static_cast<int>(threadIdx.x) % G;
+  if (j >= sq.lk || part * 8 >= p.d_real) return;
+  const int nqb = (sq.lq + 127) / 128;
+  const int left = nqb - sink_from(j / 128, p.window, sq.lk - sq.lq, nqb);
+  const int chunks = left <= 0 ? 0 : min(p.sink_chunks, (left + p.sink_len - 1) / p.sink_len);
+  const long long rows = 128ll * p.sink_tiles;
+  const long long slice = static_cast<long long>(p.B) * n_kv * rows * D;
+  const long long acc = (static_cast<long long>(bh) * rows + j) * D + part * 8;
+  const long long kr = static_cast<long long>(sq.k0) + j;
+  const long long dk_off = sq.tb * p.sdk.b + hk * p.sdk.h + kr * p.sdk.r + part * 8;
+  const long long dv_off = sq.tb * p.sdv.b + hk * p.sdv.h + kr * p.sdv.r + part * 8;
+  const int parts = (1 + chunks) * p.split;
+  if (!FA_IN_BOUNDS(p.status, acc + (parts - 1) * slice, 8, p.ext.sink) ||
+      !FA_IN_BOUNDS(p.status, dk_off, 8, p.ext.dk) || !FA_IN_BOUNDS(p.status, dv_off, 8, p.ext.dv))
+    return;
+  auto cvt = [&](const float* src, void* dst) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float4 u = reinterpret_cast<const float4*>(src + s * slice)[0];
+      const float4 t = reinterpret_cast<const float4*>(src + s * slice)[1];
+      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+      y = make_float4(y.x + t.x, y.y + t.y, y.z + t.z, y.w + t.w);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w),
+                                                pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+  };
+  cvt(p.ws_sk + acc, static_cast<__nv_bfloat16*>(p.dk) + dk_off);
+  cvt(p.ws_sv + acc, static_cast<__nv_bfloat16*>(p.dv) + dv_off);
+}
+
 // ---------------------------------------------------------------------------
 // main kernel
 // ---------------------------------------------------------------------------
@@ -362,7 +414,8 @@ __global__ void __launch_bounds__(256) bwd_kv_post_kernel(const BwdParams p) {
 // only with the direct mask walk.
 // WIN (general instances): sliding window.  Key j is seen by query i only if
 // i + off < j + window or j < sinks, so a key tile past the first `sinks` keys
-// ends its walk at the query tile of its last key's last query.
+// ends its walk at the query tile of its last key's last query; the first
+// tiles' walks go on in units of their own (BwdParams::sink_tiles).
 template <int D, bool DROPOUT, bool BITS, bool GEN = false, bool WIN = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -398,8 +451,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int Gw = G / S;             // query heads one part walks
   const int part = GEN ? static_cast<int>(unit % S) : 0;
   const int n_kv_heads = p.H / G;
-  grid_unit(GEN ? unit / S : unit, p.B * n_kv_heads, (p.rows.nk + 127) / 128, p.group_heads,
-            &w.bh, &w.kb);  // key tile 0 is heaviest
+  int chunk = -1;  // WIN: piece of a first key tile's walk past the window
+  if (WIN && unit < p.sink_units) {
+    long long u = unit / S;
+    chunk = static_cast<int>(u % p.sink_chunks);
+    u /= p.sink_chunks;
+    w.kb = static_cast<int>(u % p.sink_tiles);
+    w.bh = static_cast<int>(u / p.sink_tiles);
+  } else {
+    const long long u = WIN ? unit - p.sink_units : unit;
+    grid_unit(GEN ? u / S : u, p.B * n_kv_heads, (p.rows.nk + 127) / 128, p.group_heads,
+              &w.bh, &w.kb);  // key tile 0 is heaviest
+  }
   w.b = w.bh / n_kv_heads;
   w.hk = w.bh % n_kv_heads;
   const int hq_base = w.hk * G + part * Gw;  // first query head of this part
@@ -429,7 +492,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     w.qb_begin = 0;
   }
   if constexpr (WIN) {
-    if (w.kb * 128 >= p.sinks) {
+    if (chunk >= 0) {
+      w.qb_begin = sink_from(w.kb, p.window, w.off, w.nqb) + chunk * p.sink_len;
+      if (w.qb_begin >= w.nqb) return;  // (the whole CTA: no such piece in this sequence)
+      w.nqb = min(w.nqb, w.qb_begin + p.sink_len);
+    } else if (w.kb * 128 >= p.sinks || w.kb < p.sink_tiles) {
       const int last = w.kb * 128 + 127 + p.window - 1 - w.off;  // last query that sees a key here
       w.nqb = last < 0 ? 0 : min(w.nqb, last / 128 + 1);
     }
@@ -1152,17 +1219,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         const long long dv_off = w.tb * p.sdv.b + w.hk * p.sdv.h + kr * p.sdv.r + col;
         const long long dk_off = w.tb * p.sdk.b + w.hk * p.sdk.h + kr * p.sdk.r + col;
-        if (GEN && S > 1) {
+        if (GEN && (S > 1 || (WIN && w.kb < p.sink_tiles))) {
           // one part of a split unit: its (scaled) dK / dV go to its own fp32
           // slice ([part][tb][H_kv][key rows][D]); the conversion sums the
           // slices in part order, so the result does not depend on timing
           const long long rows_k = p.rows.cu_k == nullptr ? p.rows.nk : p.rows.total_k;
-          const long long acc =
+          long long acc =
               (((static_cast<long long>(part) * p.rows_tb + w.tb) * n_kv_heads + w.hk) * rows_k +
                kr) * D + col;
-          if (row_ok && col < p.d_real && FA_IN_BOUNDS(p.status, acc, 32, p.ext.kvacc)) {
-            float4* dvp = reinterpret_cast<float4*>(p.ws_dv + acc);
-            float4* dkp = reinterpret_cast<float4*>(p.ws_dk + acc);
+          const bool first = WIN && w.kb < p.sink_tiles;  // the first keys' own slices
+          if (first)
+            acc = ((static_cast<long long>((chunk + 1) * S + part) * p.B * n_kv_heads + w.bh) *
+                       (128ll * p.sink_tiles) + jg) * D + col;
+          if (row_ok && col < p.d_real &&
+              FA_IN_BOUNDS(p.status, acc, 32, first ? p.ext.sink : p.ext.kvacc)) {
+            float4* dvp = reinterpret_cast<float4*>((first ? p.ws_sv : p.ws_dv) + acc);
+            float4* dkp = reinterpret_cast<float4*>((first ? p.ws_sk : p.ws_dk) + acc);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float rs = p.drop_rscale, sc = p.scale;
@@ -1326,8 +1398,10 @@ cudaError_t launch_main_t(const CUtensorMap& tq, const CUtensorMap& tk, const CU
   });
   if (e != cudaSuccess) return e;
   // one unit per (b, K / V head, key tile); d = 256: two CTAs (column halves) each
-  const long long ctas = static_cast<long long>((p.rows.nk + 127) / 128) * p.B *
-                         (p.H / (GEN ? p.group : 1)) * (GEN ? p.split : 1) * (L::RING ? 2 : 1);
+  const long long ctas = (static_cast<long long>((p.rows.nk + 127) / 128) * p.B *
+                              (p.H / (GEN ? p.group : 1)) * (GEN ? p.split : 1) +
+                          (WIN ? p.sink_units : 0)) *
+                         (L::RING ? 2 : 1);
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(kern, dim3(static_cast<unsigned>(ctas)), dim3(kBwdThreads), L::SMEM,
                            stream, tq, tk, tv, tdo, tdq, p);
@@ -1401,6 +1475,17 @@ cudaError_t launch_bwd_kv_post(int d, const BwdParams& p, cudaStream_t stream) {
   if (d == 64) return launch_overlapped(bwd_kv_post_kernel<64>, grid(kRowsPerBlock<64>), dim3(256), 0, stream, p);
   if (d == 128) return launch_overlapped(bwd_kv_post_kernel<128>, grid(kRowsPerBlock<128>), dim3(256), 0, stream, p);
   if (d == 256) return launch_overlapped(bwd_kv_post_kernel<256>, grid(kRowsPerBlock<256>), dim3(256), 0, stream, p);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_bwd_sink_post(int d, const BwdParams& p, cudaStream_t stream) {
+  auto grid = [&](int rpb) {
+    return dim3(static_cast<unsigned>(128 * p.sink_tiles / rpb),
+                static_cast<unsigned>(p.B * (p.H / p.group)), 1);
+  };
+  if (d == 64) return launch_overlapped(bwd_sink_post_kernel<64>, grid(kRowsPerBlock<64>), dim3(256), 0, stream, p);
+  if (d == 128) return launch_overlapped(bwd_sink_post_kernel<128>, grid(kRowsPerBlock<128>), dim3(256), 0, stream, p);
+  if (d == 256) return launch_overlapped(bwd_sink_post_kernel<256>, grid(kRowsPerBlock<256>), dim3(256), 0, stream, p);
   return cudaErrorInvalidValue;
 }
 

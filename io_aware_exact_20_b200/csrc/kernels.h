@@ -84,7 +84,7 @@ enum : int { kStatusOk = 0, kStatusInternal = 3, kStatusTimeout = 4, kStatusBoun
 // Other builds compile the checks away (the macro drops its arguments).
 #ifdef FA_DEBUG_BOUNDS
 struct Extents {
-  long long o, lse, dout, dq, dk, dv, mask, seqlens, kvacc;
+  long long o, lse, dout, dq, dk, dv, mask, seqlens, kvacc, sink;
 };
 __device__ __forceinline__ bool in_bounds(int* status, long long off, long long width,
                                           long long extent) {
@@ -225,6 +225,16 @@ struct BwdParams {
                               // writing its dK / dV to slice p of ws_dk / ws_dv
   int rows_tb;                // batch coordinates of the tensors (B padded, 1 packed)
   int window, sinks;          // as in FwdParams
+  // Sliding window with first keys: the key tiles below sink_tiles are seen by
+  // every later query tile, so their walks past the window are cut into
+  // sink_chunks units of sink_len query tiles each, which come first in the
+  // grid (sink_units of them).  Their dK / dV, and those of the same tiles'
+  // ordinary units, are fp32 slices [1 + chunk][part][B][H_kv][128 sink_tiles][D]
+  // summed in that order.  sink_tiles = 0: every unit walks all its query tiles.
+  int sink_tiles, sink_chunks, sink_len;
+  long long sink_units;
+  float* ws_sk;
+  float* ws_sv;
   // fp32 dK / dV slices [split][rows_tb][H_kv][key rows][D] when split > 1
   float* ws_dk;
   float* ws_dv;
@@ -253,6 +263,8 @@ cudaError_t launch_bwd_main(int d, bool dropout, const CUtensorMap& tq, const CU
 cudaError_t launch_bwd_post(int d, const BwdParams& p, cudaStream_t stream);
 // dK, dV from the fp32 accumulators of split units (BwdParams::split > 1)
 cudaError_t launch_bwd_kv_post(int d, const BwdParams& p, cudaStream_t stream);
+// dK, dV of the first keys from their units' slices (BwdParams::sink_tiles > 0)
+cudaError_t launch_bwd_sink_post(int d, const BwdParams& p, cudaStream_t stream);
 
 // Fused QKV projection (fa_proj.cu): x bf16 [B N, d_model], w bf16
 // [3 H d, d_model], bias bf16 [3 H d] or null -> q, k, v bf16 [B, H, N, d].

@@ -176,3 +176,46 @@ def test_captured_and_replayed(lib):
         N, N, q.device, window=window, sinks=sinks), do)
     compare(dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv), ref)
     assert eager["o"].shape == o.shape
+
+
+@pytest.mark.parametrize("d,H,Hkv,N,window,sinks,p", [
+    (128, 4, 2, 3000, 64, 4, 0.0), (64, 3, 3, 3001, 100, 130, 0.0), (256, 2, 1, 2600, 200, 3, 0.0),
+    (96, 8, 1, 2500, 1, 257, 0.0), (64, 2, 1, 2049, 300, 1, 0.2)])
+def test_first_keys_walks_in_pieces(lib, d, H, Hkv, N, window, sinks, p):
+    """Sequences long enough that the first keys' gradients come from several
+    units; the same bits every time."""
+    q, do = randn((1, H, N, d), 70), randn((1, H, N, d), 71)
+    k, v = randn((1, Hkv, N, d), 72), randn((1, Hkv, N, d), 73)
+    keep = lib.dropout_mask(1, H, N, p, 9) if p else None
+    ref = plain64.padded(q, k, v, d ** -0.5, lambda b: plain64.visible(
+        N, N, q.device, window=window, sinks=sinks), do, keep, 1 / (1 - int(p * 65536) / 65536))
+    kw = dict(causal=True, window=window, sinks=sinks, dropout_p=p, seed=9)
+    got = run(lib, q, k, v, do, **kw)
+    compare(got, ref)
+    again = run(lib, q, k, v, do, **kw)
+    assert torch.equal(got["dk"], again["dk"]) and torch.equal(got["dv"], again["dv"])
+
+
+def test_first_keys_in_pieces_packed(lib):
+    """Sequences with and without pieces, more keys than queries and fewer, and
+    a forced split of the group."""
+    d, H, Hkv, window, sinks = 128, 4, 1, 90, 140
+    lq, lk = [2500, 1, 1400, 700, 1300], [2500, 900, 2300, 30, 1100]
+    cq, ck = [0] + torch.tensor(lq).cumsum(0).tolist(), [0] + torch.tensor(lk).cumsum(0).tolist()
+    q, do = randn((cq[-1], H, d), 80), randn((cq[-1], H, d), 81)
+    k, v = randn((ck[-1], Hkv, d), 82), randn((ck[-1], Hkv, d), 83)
+    kw = dict(layout="thd", cu_seqlens_q=cq, cu_seqlens_k=ck, max_seqlen_q=max(lq), max_seqlen_k=max(lk),
+              causal=True, window=window, sinks=sinks)
+    for parts in (0, 1, 2):
+        lib.set_gqa_split(parts)
+        try:
+            r = run(lib, q, k, v, do, **kw)
+        finally:
+            lib.set_gqa_split(0)
+        for b, (n, m) in enumerate(zip(lq, lk)):
+            rq, rk = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b + 1])
+            part = lambda t, s: t[s].transpose(0, 1)[None]  # noqa: E731
+            ref = plain64.padded(part(q, rq), part(k, rk), part(v, rk), d ** -0.5,
+                                 lambda _: plain64.visible(n, m, q.device, window=window, sinks=sinks), part(do, rq))
+            compare(dict(o=part(r["o"], rq), dq=part(r["dq"], rq), dk=part(r["dk"], rk), dv=part(r["dv"], rk),
+                         lse=r["lse"][:, rq][None]), ref)
