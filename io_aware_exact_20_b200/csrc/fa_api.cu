@@ -456,7 +456,11 @@ fa_status_t bwd_params(fa::BwdParams* p, const Problem& pr, const void* workspac
   p->window = pr.window;
   p->sinks = pr.sinks;
   p->d_real = pr.d;
-  p->scale = pr.scale;
+  // A window of the query's own key alone: its probability is 1 whatever the
+  // score, so dQ and dK are exactly 0; dP - D would leave rounding noise there.
+  // (This scale is only the final factor of dQ and dK.)
+  const bool own_key_only = pr.window == 1 && pr.sinks == 0;
+  p->scale = own_key_only ? 0.f : pr.scale;
   p->scale_log2 = static_cast<float>(static_cast<double>(pr.scale) * kLog2e);
   p->causal = pr.causal;
   // the main kernel's units are (b, K / V head, key tile): its head groups are

@@ -219,3 +219,15 @@ def test_first_keys_in_pieces_packed(lib):
                                  lambda _: plain64.visible(n, m, q.device, window=window, sinks=sinks), part(do, rq))
             compare(dict(o=part(r["o"], rq), dq=part(r["dq"], rq), dk=part(r["dk"], rk), dv=part(r["dv"], rk),
                          lse=r["lse"][:, rq][None]), ref)
+
+
+@pytest.mark.parametrize("d,Hkv,p", [(64, 2, 0.0), (128, 1, 0.0), (64, 1, 0.25), (256, 2, 0.0)])
+def test_own_key_alone_has_no_score_gradient(lib, d, Hkv, p):
+    """Window 1 without first tokens: O is V's row, dQ and dK are exactly zero, dV is dO."""
+    H, N = 2, 300
+    q, do = randn((1, H, N, d), 90), randn((1, H, N, d), 91)
+    k, v = randn((1, Hkv, N, d), 92), randn((1, Hkv, N, d), 93)
+    got = run(lib, q, k, v, do, causal=True, window=1, dropout_p=p, seed=3)
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+    if not p:
+        assert torch.equal(got["o"], v.repeat_interleave(H // Hkv, 1))
