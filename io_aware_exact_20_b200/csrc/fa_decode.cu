@@ -238,26 +238,32 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
   const uint32_t ring = smem_u32(smem) + warp * C::WARP;
   uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
 
+  if (p.c.d < D)
+    for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
+  __syncwarp();
+
   uint32_t chunk_lo = 0;  // tile at which this chunk of sequences begins
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     if (p.batch > kThreads) part = scan(load_seq(b0 + threadIdx.x));  // else it is still there
-    // rows without keys belong to no share: the last block writes them
+    // rows without keys belong to no share: the last block's warps write theirs
     if (blockIdx.x == gridDim.x - 1) {
-      for (int j = 0; j < min(kThreads, p.batch - b0); ++j) {
-        if (sq.tiles[j] != 0) continue;
-        const int b = b0 + j;
-        for (int x = threadIdx.x; x < p.heads * (p.c.d / 8); x += kThreads) {
+      uint32_t none = __ballot_sync(0xffffffffu, b0 + static_cast<int>(threadIdx.x) < p.batch &&
+                                                     sq.tiles[threadIdx.x] == 0);
+      for (; none != 0u; none &= none - 1u) {
+        const int b = b0 + 32 * warp + __ffs(none) - 1;
+        for (int x = lane; x < p.heads * (p.c.d / 8); x += 32) {
           const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
           *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
           if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
         }
         if (p.cut_rows != nullptr)
-          for (int x = threadIdx.x; x < rows_per_seq; x += kThreads)
+          for (int x = lane; x < rows_per_seq; x += 32)
             p.cut_rows[static_cast<long long>(b) * rows_per_seq + x] = make_int2(0, 0);
       }
     }
     const uint32_t chunk_hi = chunk_lo + part * rows_per_seq;
-    const uint32_t from = max(lo, chunk_lo), end = min(hi, chunk_hi);
+    const uint32_t from = max(lo, chunk_lo);
+    uint32_t end = min(hi, chunk_hi), step = 1;
     if (from < end) {
       // the row of tile `from`: the first sequence whose running sum passes it
       Cursor at;
@@ -278,8 +284,18 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         at.hi = at.lo + tiles;
         at.f = from;
       }
-      auto advance = [&](Cursor& c) {  // one tile on; c.f < end afterwards or the cursor is not used
-        if (++c.f < c.hi || c.f >= end) return;
+      // Where the block's four shares lie in one row its warps take turns, so that
+      // they read neighbouring rows at a time, and their parts meet at the end.
+      const bool block_row = full && at.lo <= blk_lo && at.hi >= blk_hi;
+      if (block_row) {
+        at.f = blk_lo + warp;
+        end = blk_hi;
+        step = kWarps;
+      }
+      const uint32_t first = at.f;
+      auto advance = [&](Cursor& c) {  // a tile on; c.f < end afterwards or the cursor is not used
+        c.f += step;
+        if (c.f < c.hi || c.f >= end) return;
         if (++c.rs == rows_per_seq) {
           c.rs = 0;
           do ++c.j;
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
       auto locate = [&](const Cursor& c) -> Key {
         Key r{-1, 0, c.hk};
         if (c.f >= end) return r;
-        if (c.f == c.lo || c.f == from) {
+        if (c.f == c.lo || c.f == first) {
           // a row begins: its Q into L2, a 128-byte line a lane
           const int hb = c.rs - c.hk * p.head_blocks, lines = (2 * p.c.d + 127) / 128;
           const int h = lane / lines;
@@ -324,29 +340,53 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
         const uint32_t live = __ballot_sync(0xffffffffu, r.page >= 0 && r.page < p.c.pages);
         if (lane == 0) valid[stage] = live;
-        const bool col_ok = 8 * c < p.c.d;
+        const bool col_ok = 8 * c < p.c.d;  // past d the ring holds zeros
         const __nv_bfloat16* kh = p.k + r.hk * p.c.k_head + 8 * c;
         const __nv_bfloat16* vh = p.v + r.hk * p.c.v_head + 8 * c;
+        // Most tiles are one run of consecutive rows, or two (where the tile crosses
+        // a page, or from the first tokens into the window): one or two places to
+        // start from instead of one per row.  (With two places for every tile, d =
+        // 256 took 119 us where it takes 93.)
+        const int x = lane & (KT - 1);
         const int page0 = __shfl_sync(0xffffffffu, r.page, 0), row0 = __shfl_sync(0xffffffffu, r.row, 0);
-        if (__all_sync(0xffffffffu, r.page == page0 && r.row == row0 + (lane & (KT - 1)) && col_ok) &&
-            (live & 1u)) {
-          // consecutive rows of one page
-          const __nv_bfloat16* kp = kh + page0 * p.c.k_page + (row0 + lane / CH) * p.c.k_row;
-          const __nv_bfloat16* vp = vh + page0 * p.c.v_page + (row0 + lane / CH) * p.c.v_row;
+        const uint32_t other = __ballot_sync(0xffffffffu, r.page != page0 || r.row != row0 + x);
+        const bool all_live = live == 0xffffffffu;
+        const int row_l = lane / CH;
+        const __nv_bfloat16* k0 = kh + page0 * p.c.k_page + (row0 + row_l) * p.c.k_row;
+        const __nv_bfloat16* v0 = vh + page0 * p.c.v_page + (row0 + row_l) * p.c.v_row;
+        if (all_live && other == 0u) {
 #pragma unroll
           for (int s = 0; s < KT / RPI; ++s) {
-            const int row = s * RPI + lane / CH;
+            const int row = s * RPI + row_l;
             const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
-            cp_async16(kdst + dst, kp + s * RPI * p.c.k_row, true);
-            cp_async16(vdst + dst, vp + s * RPI * p.c.v_row, true);
+            if (!col_ok) break;
+            cp_async16(kdst + dst, k0 + s * RPI * p.c.k_row, true);
+            cp_async16(vdst + dst, v0 + s * RPI * p.c.v_row, true);
+          }
+          return;
+        }
+        const int cut = other ? __ffs(other) - 1 : 0;  // first row of the second run
+        const int page1 = __shfl_sync(0xffffffffu, r.page, cut);
+        const int row1 = __shfl_sync(0xffffffffu, r.row, cut) - cut;
+        if (__all_sync(0xffffffffu, all_live && (x < cut || (r.page == page1 && r.row == row1 + x)))) {
+          const __nv_bfloat16* k1 = kh + page1 * p.c.k_page + (row1 + row_l) * p.c.k_row;
+          const __nv_bfloat16* v1 = vh + page1 * p.c.v_page + (row1 + row_l) * p.c.v_row;
+#pragma unroll
+          for (int s = 0; s < KT / RPI; ++s) {
+            const int row = s * RPI + row_l;
+            const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+            if (!col_ok) break;
+            cp_async16(kdst + dst, (row < cut ? k0 : k1) + s * RPI * p.c.k_row, true);
+            cp_async16(vdst + dst, (row < cut ? v0 : v1) + s * RPI * p.c.v_row, true);
           }
         } else {
 #pragma unroll
           for (int s = 0; s < KT / RPI; ++s) {
             const int row = s * RPI + lane / CH;
             const int page = __shfl_sync(0xffffffffu, r.page, row), at_row = __shfl_sync(0xffffffffu, r.row, row);
-            const bool ok = col_ok && ((live >> row) & 1u);
+            const bool ok = (live >> row) & 1u;
             const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+            if (!col_ok) continue;
             cp_async16(kdst + dst, ok ? kh + page * p.c.k_page + at_row * p.c.k_row : p.k, ok);
             cp_async16(vdst + dst, ok ? vh + page * p.c.v_page + at_row * p.c.v_row : p.v, ok);
           }
@@ -363,14 +403,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         }
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
-          if (at.f + s < end) load(s, ahead[s]);
+          if (at.f + s * step < end) load(s, ahead[s]);
           cp_async_commit();
         }
       }
       Key next = locate(fill);
 
-      // whether the block's four shares lie in one row
-      const bool block_row = full && at.lo <= blk_lo && at.hi >= blk_hi;
       uint32_t qa[C::Q_SMEM ? 1 : D / 16][4];  // Q as the A operand: rows g and g + 8
       const uint32_t qs = smem_u32(smem) + C::OFF_Q + warp * 16 * C::ROW;
       float o[D / 8][4];
@@ -511,7 +549,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         stage = stage + 1 == STAGES ? 0 : stage + 1;
 
         const uint32_t f1 = at.f + 1;
-        if (block_row && f1 == end) {
+        if (block_row) {
+          if (at.f + step < end) {
+            advance(at);
+            continue;
+          }
           // all of the block's shares are parts of this row: they meet below
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -604,7 +646,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
               p.part_stat[2ll * (blk0 + w) * 16 + r] = make_float2(-INFINITY, 0.f);
           }
         }
-        if (p.batch > kThreads) __syncthreads();
+        if (p.batch > kThreads) {
+          __syncthreads();
+          if (p.c.d < D)  // the ring held fp32 sums
+            for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
+          __syncwarp();
+        }
       }
     }
     chunk_lo = chunk_hi;
@@ -712,7 +759,7 @@ struct Plan {
 Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const int D = c.d <= 64 ? 64 : c.d <= 128 ? 128 : 256;
   const int KT = D == 64 ? DecodeCfg<64>::KT : D == 128 ? DecodeCfg<128>::KT : DecodeCfg<256>::KT;
-  const int per_sm = D == 256 ? DecodeCfg<256>::MIN_BLOCKS : DecodeCfg<128>::MIN_BLOCKS;
+  const int per_sm = D == 64 ? DecodeCfg<64>::MIN_BLOCKS : D == 128 ? DecodeCfg<128>::MIN_BLOCKS : DecodeCfg<256>::MIN_BLOCKS;
   long long most = static_cast<long long>(c.max_pages) * c.page_size;
   if (window > 0 && static_cast<long long>(window) + sinks < most) most = static_cast<long long>(window) + sinks;
   const long long tiles = (most + KT - 1) / KT;
