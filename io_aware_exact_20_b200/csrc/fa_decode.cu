@@ -4,12 +4,17 @@
 // attend the visible keys in one pass: S = Q K^T, the running row maximum and
 // sum of the online softmax, O += P V.  Every K / V row is read once from
 // memory and serves the whole group, 2 G operations per byte, so the kernel is
-// bound by memory bandwidth as long as the arithmetic keeps out of the way:
-// the products run on warp-level bf16 matrix instructions (m16n8k16; the 16
-// rows are the group's heads, so a 128-row tcgen05 tile would be 7/8 or more
-// padding and would need the scores to leave TMEM for one row in eight), and
-// every warp works on its own tiles of KT keys with its own ring of
-// asynchronous copies, so that no warp waits for another before the end.
+// bound by memory bandwidth as long as the arithmetic keeps out of the way.
+// The products are transposed, S^T = K Q^T and O^T = V^T P^T, on warp-level bf16
+// matrix instructions (m16n8k16): the 16 rows are keys, or columns of V, and the
+// 8 columns the group's heads (twice 8 for groups of 9 and more), so a group
+// of up to 8 heads wastes at most its padding to 8.  (With the heads as the 16
+// rows, half the instructions of a group of 4 worked on padding and the
+// accumulators left registers for two warps per scheduler, which then waited
+// for their own instructions more than for memory; a 128-row tcgen05 tile would
+// be nearly all padding.)  Every warp works on its own tiles of KT keys with
+// its own ring of asynchronous copies, so that no warp waits for another before
+// the end.
 //
 // The work is cut evenly whatever the lengths are: each (sequence, K / V head,
 // block of heads) is a row of tiles, the rows of the batch lie end to end, and
@@ -48,7 +53,8 @@ struct AttendParams {
   long long q_batch, q_head, o_batch, o_head;
   const int32_t* slots;
   int batch, heads, group;
-  int head_blocks;   // blocks of up to 16 query heads per K / V head
+  int block_heads;   // query heads of a row: 8, or 16 where a K / V head has more than 8
+  int head_blocks;   // rows per K / V head
   float scale_log2;  // softmax_scale * log2(e)
   int window, sinks;
   // partial results of the shares, null where no row can be cut
@@ -88,6 +94,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Transpose of an 8 x 8 matrix of bf16 held as pairs: (row g, columns 2 q4,
+// 2 q4 + 1) in, (column g, rows 2 q4, 2 q4 + 1) out.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Sum over the eight rows of a column: the lanes with the same q4.
+__device__ __forceinline__ float sum_rows(float x) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
 // Asks for a line that will be read soon.
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -95,7 +114,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 
 constexpr int kWarps = 4;
 
-template <int D>
+// D: head dim in the kernel, NB: blocks of 8 query heads of a row.
+template <int D, int NB>
 struct DecodeCfg {
   static constexpr int KT = D == 64 ? 32 : 16;   // keys of a warp's tile
   static constexpr int STAGES = 3;               // tiles in a warp's ring
@@ -103,10 +123,7 @@ struct DecodeCfg {
   static constexpr uint32_t STAGE = 2 * KT * ROW;  // K then V
   static constexpr uint32_t WARP = STAGES * STAGE;
   static constexpr uint32_t OFF_VALID = kWarps * WARP;  // [warp][stage] key bits
-  // Q: registers, but at D = 256, where O fills them, a tile of 16 rows per warp
-  static constexpr bool Q_SMEM = D == 256;
-  static constexpr uint32_t OFF_Q = (OFF_VALID + kWarps * STAGES * 4 + 127) / 128 * 128;
-  static constexpr uint32_t SMEM = OFF_Q + (Q_SMEM ? kWarps * 16 * ROW : 0);
+  static constexpr uint32_t SMEM = OFF_VALID + kWarps * STAGES * 4;
   static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
 };
 
@@ -170,9 +187,10 @@ struct Cursor {
   int j, rs, hk;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_kernel(const AttendParams p) {
-  using C = DecodeCfg<D>;
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
+    attend_kernel(const AttendParams p) {
+  using C = DecodeCfg<D, NB>;
   constexpr int KT = C::KT, STAGES = C::STAGES;
   griddep_wait();
   griddep_launch_dependents();
@@ -180,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
   __shared__ Seqs sq;
   const uint32_t warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int g = lane >> 2, q4 = lane & 3;  // row and column group of the matrix fragments
+  const int g = lane >> 2, q4 = lane & 3;  // row, and pair of columns, of the matrix fragments
+  constexpr int HB = 8 * NB;               // query heads of a row
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
 
   // ---- the shares: tiles of every sequence, their sum and this warp's part
@@ -319,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           // a row begins: its Q into L2, a 128-byte line a lane
           const int hb = c.rs - c.hk * p.head_blocks, lines = (2 * p.c.d + 127) / 128;
           const int h = lane / lines;
-          if (h < min(16, p.group - hb * 16))
-            prefetch_l2(p.q + (b0 + c.j) * p.q_batch + (c.hk * p.group + hb * 16 + h) * p.q_head +
+          if (h < min(HB, p.group - hb * HB))
+            prefetch_l2(p.q + (b0 + c.j) * p.q_batch + (c.hk * p.group + hb * HB + h) * p.q_head +
                         (lane - h * lines) * 64);
         }
         const Visible vis = visible_of(sq.len[c.j], p.window, p.sinks);
@@ -409,10 +428,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
       }
       Key next = locate(fill);
 
-      uint32_t qa[C::Q_SMEM ? 1 : D / 16][4];  // Q as the A operand: rows g and g + 8
-      const uint32_t qs = smem_u32(smem) + C::OFF_Q + warp * 16 * C::ROW;
-      float o[D / 8][4];
-      float m[2], l[2];           // rows g, g + 8; l: this lane's part
+      uint32_t qb[NB][D / 16][2];  // Q as the B operand: column g is a head
+      float o[NB][D / 16][4];      // O^T: rows g, g + 8 of 16 columns of V; heads 2 q4, 2 q4 + 1
+      float m[NB][2], l[NB][2];    // of those heads; l: this lane's keys alone
       bool begin = true;
       int stage = 0;
       while (at.f < end) {
@@ -423,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         advance(fill);
         next = locate(fill);
         const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
-        const int h0 = hk * p.group + hb * 16;      // first query head of the row
-        const int hn = min(16, p.group - hb * 16);  // its query heads
+        const int h0 = hk * p.group + hb * HB;      // first query head of the row
+        const int hn = min(HB, p.group - hb * HB);  // its query heads
         const int b = b0 + at.j;
         if (begin) {
           // the joining kernel learns the row's shares from the one it begins in
@@ -433,119 +451,119 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
                 make_int2(share, at.hi <= hi ? share : sh.holding(at.hi - 1));
           // Q: zero past the row's heads and past d
           const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
-          if constexpr (C::Q_SMEM) {
 #pragma unroll
-            for (int x = lane; x < 16 * (D / 8); x += 32) {
-              const int r = x / (D / 8), c = x % (D / 8);
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (r < hn && 8 * c < p.c.d) v = *reinterpret_cast<const uint4*>(q0 + r * p.q_head + 8 * c);
-              st_shared_v4(qs + r * C::ROW + ((c ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-            }
-          } else {
+          for (int nb = 0; nb < NB; ++nb) {
+            const int h = 8 * nb + g;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int r = g + 8 * (u & 1), col = 16 * kk + 8 * (u >> 1) + 2 * q4;
-                qa[kk][u] = r < hn && col < p.c.d
-                                ? *reinterpret_cast<const uint32_t*>(q0 + r * p.q_head + col)
-                                : 0u;
+              for (int u = 0; u < 2; ++u) {
+                const int col = 16 * kk + 8 * u + 2 * q4;
+                qb[nb][kk][u] = h < hn && col < p.c.d
+                                    ? *reinterpret_cast<const uint32_t*>(q0 + h * p.q_head + col)
+                                    : 0u;
               }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) o[nb][i][u] = 0.f;
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.f;
           }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) o[i][u] = 0.f;
-          m[0] = m[1] = -INFINITY;
-          l[0] = l[1] = 0.f;
           begin = false;
         }
         cp_async_wait<STAGES - 1>();
         __syncwarp();
         const uint32_t kbase = ring + stage * C::STAGE, vbase = kbase + KT * C::ROW;
         const uint32_t live = valid[stage];
+        constexpr int MT = KT / 16;  // 16-key rows of S^T
         // two sums per score, over the even and the odd steps: half the chain
-        float s[KT / 8][4], s1[KT / 8][4];
+        float s[MT][NB][4], s1[MT][NB][4];
 #pragma unroll
-        for (int i = 0; i < KT / 8; ++i)
+        for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) s[i][u] = s1[i][u] = 0.f;
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          if constexpr (C::Q_SMEM)
-            ldsm_x4(qs + (lane & 15) * C::ROW + (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4), qa[0]);
-          const uint32_t(&qk)[4] = qa[C::Q_SMEM ? 0 : kk];
+            for (int u = 0; u < 4; ++u) s[kt][nb][u] = s1[kt][nb][u] = 0.f;
 #pragma unroll
-          for (int kt = 0; kt < KT / 16; ++kt) {
-            uint32_t kb[4];
-            const int row = kt * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
-            const int ch = 2 * kk + ((lane >> 3) & 1);
-            ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), kb);
-            mma16816(kk & 1 ? s1[2 * kt] : s[2 * kt], qk, kb[0], kb[1]);
-            mma16816(kk & 1 ? s1[2 * kt + 1] : s[2 * kt + 1], qk, kb[2], kb[3]);
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int kt = 0; kt < MT; ++kt) {
+            uint32_t ka[4];
+            const int row = kt * 16 + (lane & 15), ch = 2 * kk + (lane >> 4);
+            ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), ka);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816(kk & 1 ? s1[kt][nb] : s[kt][nb], ka, qb[nb][kk][0], qb[nb][kk][1]);
           }
-        }
 #pragma unroll
-        for (int i = 0; i < KT / 8; ++i)
+        for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) s[i][u] += s1[i][u];
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[kt][nb][u] += s1[kt][nb][u];
         constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
         if ((live & kAll) != kAll) {
 #pragma unroll
-          for (int i = 0; i < KT / 8; ++i)
+          for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              s[i][u] = (live >> (8 * i + 2 * q4 + (u & 1))) & 1u ? s[i][u] : -INFINITY;
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                s[kt][nb][u] = (live >> (16 * kt + g + 8 * (u >> 1))) & 1u ? s[kt][nb][u] : -INFINITY;
         }
-        float alpha[2];
+        // Online softmax over the tile's keys, per head of this lane's pair; P is
+        // rounded to bf16 for the second product, as in the other attention
+        // kernels, and turned from rows of keys to columns (the B operand); the
+        // row sum keeps the unrounded values
+        uint32_t pb[NB][MT][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float mx = -INFINITY;
+        for (int nb = 0; nb < NB; ++nb) {
+          float alpha[2];
 #pragma unroll
-          for (int i = 0; i < KT / 8; ++i) mx = fmax3(mx, s[i][2 * r], s[i][2 * r + 1]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float m_new = fmaxf(m[r], mx * p.scale_log2);
-          const float ref = m_new == -INFINITY ? 0.f : m_new;
-          alpha[r] = fast_exp2(m[r] - ref);
-          m[r] = m_new;
-          float rs = 0.f;
+          for (int u = 0; u < 2; ++u) {
+            float mx = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < KT / 8; ++i)
+            for (int kt = 0; kt < MT; ++kt) mx = fmax3(mx, s[kt][nb][u], s[kt][nb][u + 2]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float e = fast_exp2(fmaf(s[i][2 * r + u], p.scale_log2, -ref));
-              s[i][2 * r + u] = e;
-              rs += e;
-            }
-          l[r] = l[r] * alpha[r] + rs;
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float m_new = fmaxf(m[nb][u], mx * p.scale_log2);
+            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            alpha[u] = fast_exp2(m[nb][u] - ref);
+            m[nb][u] = m_new;
+            float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= alpha[0];
-            o[i][1] *= alpha[0];
-            o[i][2] *= alpha[1];
-            o[i][3] *= alpha[1];
+            for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float e = fast_exp2(fmaf(s[kt][nb][u + 2 * r], p.scale_log2, -ref));
+                s[kt][nb][u + 2 * r] = e;
+                sum += e;
+              }
+            l[nb][u] = l[nb][u] * alpha[u] + sum;
           }
-        }
-        // P is rounded to bf16 for the second product, as in the other attention
-        // kernels; the row sum keeps the unrounded values
+          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-        for (int kt = 0; kt < KT / 16; ++kt) {
-          const uint32_t pa[4] = {pack_bf16(s[2 * kt][0], s[2 * kt][1]), pack_bf16(s[2 * kt][2], s[2 * kt][3]),
-                                  pack_bf16(s[2 * kt + 1][0], s[2 * kt + 1][1]),
-                                  pack_bf16(s[2 * kt + 1][2], s[2 * kt + 1][3])};
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) o[nb][i][u] *= alpha[u & 1];
+          }
+#pragma unroll
+          for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              pb[nb][kt][r] = transpose8x8(pack_bf16(s[kt][nb][2 * r], s[kt][nb][2 * r + 1]));
+        }
+#pragma unroll
+        for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
           for (int dd = 0; dd < D / 16; ++dd) {
-            uint32_t vb[4];
-            const int row = kt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-            const int ch = 2 * dd + (lane >> 4);
-            ldsm_x4_trans(vbase + row * C::ROW + ((ch ^ (row & 7)) << 4), vb);
-            mma16816(o[2 * dd], pa, vb[0], vb[1]);
-            mma16816(o[2 * dd + 1], pa, vb[2], vb[3]);
+            uint32_t va[4];
+            const int row = kt * 16 + (lane & 7) + (lane >> 4) * 8, ch = 2 * dd + ((lane >> 3) & 1);
+            ldsm_x4_trans(vbase + row * C::ROW + ((ch ^ (row & 7)) << 4), va);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][dd], va, pb[nb][kt][0], pb[nb][kt][1]);
           }
-        }
         stage = stage + 1 == STAGES ? 0 : stage + 1;
 
         const uint32_t f1 = at.f + 1;
@@ -554,12 +572,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
             advance(at);
             continue;
           }
-          // all of the block's shares are parts of this row: they meet below
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-          }
+          break;  // the warps' parts of this row meet below
         } else if (f1 == at.hi || f1 == end) {
           // the row ends, or the share: the whole row goes to O and LSE, a part of
           // it to the share's partial results, index 1 where the row begins in
@@ -567,27 +580,45 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
           const bool begins = at.lo >= lo, whole = begins && f1 == at.hi;
           const long long pr = (2ll * share + (begins ? 1 : 0)) * 16;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            const int row = g + 8 * r;
-            if (row >= hn) continue;
+          for (int nb = 0; nb < NB; ++nb) {
+            float inv[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              l[nb][u] = sum_rows(l[nb][u]);
+              inv[u] = l[nb][u] > 0.f ? 1.f / l[nb][u] : 0.f;
+              const int h = 8 * nb + 2 * q4 + u;
+              if (g == 0 && h < hn) {
+                if (whole)
+                  p.lse[static_cast<long long>(b) * p.heads + h0 + h] =
+                      l[nb][u] > 0.f ? (m[nb][u] + log2f(l[nb][u])) * kLn2 : -INFINITY;
+                else
+                  p.part_stat[pr + h] = make_float2(m[nb][u], l[nb][u]);
+              }
+            }
             if (whole) {
-              const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-              __nv_bfloat16* dst = p.o + b * p.o_batch + (h0 + row) * p.o_head + 2 * q4;
+              // pairs of columns of V for head g, out of pairs of heads
+              __nv_bfloat16* dst = p.o + b * p.o_batch + (h0 + 8 * nb + g) * p.o_head + 2 * q4;
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                if (8 * i < p.c.d)
-                  *reinterpret_cast<uint32_t*>(dst + 8 * i) = pack_bf16(o[i][2 * r] * inv, o[i][2 * r + 1] * inv);
-              if (q4 == 0)
-                p.lse[static_cast<long long>(b) * p.heads + h0 + row] =
-                    l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t x =
+                      transpose8x8(pack_bf16(o[nb][i][2 * r] * inv[0], o[nb][i][2 * r + 1] * inv[1]));
+                  const int col = 16 * i + 8 * r;
+                  if (8 * nb + g < hn && col < p.c.d) *reinterpret_cast<uint32_t*>(dst + col) = x;
+                }
             } else {
-              float* dst = p.part_acc + (pr + row) * D + 2 * q4;
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-              if (q4 == 0) p.part_stat[pr + row] = make_float2(m[r], l[r]);
+              for (int u = 0; u < 2; ++u) {
+                const int h = 8 * nb + 2 * q4 + u;
+                float* dst = p.part_acc + (pr + h) * D + g;
+                if (h < hn)
+#pragma unroll
+                  for (int i = 0; i < D / 16; ++i) {
+                    dst[16 * i] = o[nb][i][u];
+                    dst[16 * i + 8] = o[nb][i][2 + u];
+                  }
+              }
             }
           }
           begin = true;
@@ -599,40 +630,44 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
         // one partial result for the block, in its first share's place (the
         // others' stay empty): a quarter of what the joining kernel would read
         const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
-        const int hn = min(16, p.group - hb * 16);
+        const int hn = min(HB, p.group - hb * HB);
+        constexpr int LD = D + 4;  // (a warp's eight heads in different banks)
         __syncthreads();
-        float2* stat = reinterpret_cast<float2*>(smem);  // [warp][16], then [warp][16][D] sums
-        float* acc = reinterpret_cast<float*>(smem + kWarps * 16 * sizeof(float2));
-        if (q4 == 0) {
-          stat[warp * 16 + g] = make_float2(m[0], l[0]);
-          stat[warp * 16 + g + 8] = make_float2(m[1], l[1]);
-        }
+        float2* stat = reinterpret_cast<float2*>(smem);  // [warp][HB], then [warp][HB][LD] sums
+        float* acc = reinterpret_cast<float*>(smem + kWarps * HB * sizeof(float2));
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          float* a = acc + (warp * 16 + g) * D + 8 * i + 2 * q4;
-          *reinterpret_cast<float2*>(a) = make_float2(o[i][0], o[i][1]);
-          *reinterpret_cast<float2*>(a + 8 * D) = make_float2(o[i][2], o[i][3]);
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int h = warp * HB + 8 * nb + 2 * q4 + u;
+            const float sum = sum_rows(l[nb][u]);
+            if (g == 0) stat[h] = make_float2(m[nb][u], sum);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              acc[h * LD + 16 * i + g] = o[nb][i][u];
+              acc[h * LD + 16 * i + 8 + g] = o[nb][i][2 + u];
+            }
+          }
         __syncthreads();
         const bool begins = at.lo >= blk_lo, whole = begins && at.hi == blk_hi;
         for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
           const int r = x / (D / 8), col = 8 * (x % (D / 8));
           float mm = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * 16 + r].x);
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * HB + r].x);
           const float ref = mm == -INFINITY ? 0.f : mm;
           float rs = 0.f, out[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) out[e] = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 st = stat[w * 16 + r];
+            const float2 st = stat[w * HB + r];
             const float f = fast_exp2(st.x - ref);
             rs += f * st.y;
-            add_row8(out, f, acc + (w * 16 + r) * D + col);
+            add_row8(out, f, acc + (w * HB + r) * LD + col);
           }
           if (whole) {
-            if (col < p.c.d) write_row(p, b0 + at.j, hk * p.group + hb * 16 + r, col, mm, rs, out);
+            if (col < p.c.d) write_row(p, b0 + at.j, hk * p.group + hb * HB + r, col, mm, rs, out);
             continue;
           }
           const long long row = (2ll * blk0 + (begins ? 1 : 0)) * 16 + r;
@@ -665,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::MIN_BLOCKS) attend_ker
 // parts, whose loads wait for nothing (with the maximum carried from part to
 // part, 16 rows of 37 parts at d = 256 took 13 us).
 constexpr int kJoinThreads = 256, kJoinHeads = 4;
-constexpr int kJoinParts = 148 * 2 * kWarps;  // a row has no more shares than a grid has warps
+constexpr int kJoinParts = 148 * 4 * kWarps;  // a row has no more shares than a grid has warps
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
@@ -681,7 +716,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
   const int b = blockIdx.x / rows_per_seq, rs = blockIdx.x - b * rows_per_seq;
   const int hk = rs / p.head_blocks, hb = rs - hk * p.head_blocks;
-  const int hn = min(16, p.group - hb * 16) - blockIdx.y * kJoinHeads;  // this block's heads, and more
+  const int HB = p.block_heads;
+  const int hn = min(HB, p.group - hb * HB) - blockIdx.y * kJoinHeads;  // this block's heads, and more
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // partial result i of head r of this block (see attend_kernel)
   auto row_of = [&](int i, int r) {
@@ -742,7 +778,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     mm = fmaxf(mm, red[w][r].x);
     all += red[w][r].y;
   }
-  write_row(p, b, hk * p.group + hb * 16 + blockIdx.y * kJoinHeads + r, col, mm, all, out);
+  write_row(p, b, hk * p.group + hb * HB + blockIdx.y * kJoinHeads + r, col, mm, all, out);
 }
 
 // Grid and workspace of a call, from what the host knows: the longest that a
@@ -756,14 +792,27 @@ struct Plan {
   size_t off_stat, off_acc, bytes;
 };
 
+template <int NB>
+void sizes_of(int D, int* KT, int* per_sm) {
+  *KT = D == 64 ? DecodeCfg<64, NB>::KT : D == 128 ? DecodeCfg<128, NB>::KT : DecodeCfg<256, NB>::KT;
+  *per_sm = D == 64    ? DecodeCfg<64, NB>::MIN_BLOCKS
+            : D == 128 ? DecodeCfg<128, NB>::MIN_BLOCKS
+                       : DecodeCfg<256, NB>::MIN_BLOCKS;
+}
+
+// Query heads of a row for a group of G per K / V head.
+int block_heads_of(int G) { return G <= 8 ? 8 : 16; }
+
 Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const int D = c.d <= 64 ? 64 : c.d <= 128 ? 128 : 256;
-  const int KT = D == 64 ? DecodeCfg<64>::KT : D == 128 ? DecodeCfg<128>::KT : DecodeCfg<256>::KT;
-  const int per_sm = D == 64 ? DecodeCfg<64>::MIN_BLOCKS : D == 128 ? DecodeCfg<128>::MIN_BLOCKS : DecodeCfg<256>::MIN_BLOCKS;
+  const int G = heads / c.heads_kv, HB = block_heads_of(G);
+  int KT = 0, per_sm = 0;
+  if (HB == 8) sizes_of<1>(D, &KT, &per_sm);
+  else sizes_of<2>(D, &KT, &per_sm);
   long long most = static_cast<long long>(c.max_pages) * c.page_size;
   if (window > 0 && static_cast<long long>(window) + sinks < most) most = static_cast<long long>(window) + sinks;
   const long long tiles = (most + KT - 1) / KT;
-  const long long rows = static_cast<long long>(batch) * c.heads_kv * ((heads / c.heads_kv + 15) / 16);
+  const long long rows = static_cast<long long>(batch) * c.heads_kv * ((G + HB - 1) / HB);
   Plan p;
   p.tiles = rows * tiles;
   p.grid = p.tiles < 148ll * per_sm ? p.tiles : 148ll * per_sm;
@@ -775,11 +824,11 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   return p;
 }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t stream) {
-  using C = DecodeCfg<D>;
-  static_assert(kWarps * 16 * (8 + D * 4) <= C::OFF_VALID, "a block's parts fit the ring");
-  auto kern = attend_kernel<D>;
+  using C = DecodeCfg<D, NB>;
+  static_assert(kWarps * 8 * NB * (8 + (D + 4) * 4) <= C::OFF_VALID, "a block's parts fit the ring");
+  auto kern = attend_kernel<D, NB>;
   static OncePerContext prepared;
   const cudaError_t e = prepared.run([&]() -> cudaError_t {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -799,7 +848,7 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
   if (r == cudaSuccess && plan.cut)
     r = launch_overlapped(join_kernel<D>,
                           dim3(static_cast<unsigned>(p.batch * p.c.heads_kv * p.head_blocks),
-                               static_cast<unsigned>(((p.group < 16 ? p.group : 16) + kJoinHeads - 1) / kJoinHeads)),
+                               static_cast<unsigned>(((p.group < p.block_heads ? p.group : p.block_heads) + kJoinHeads - 1) / kJoinHeads)),
                           dim3(kJoinThreads), 0, stream, a);
   return r;
 }
@@ -855,7 +904,8 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.batch = batch;
   p.heads = heads;
   p.group = heads / p.c.heads_kv;
-  p.head_blocks = (p.group + 15) / 16;
+  p.block_heads = fa::block_heads_of(p.group);
+  p.head_blocks = (p.group + p.block_heads - 1) / p.block_heads;
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * fa::kLog2e);
   p.window = window;
   p.sinks = sinks;
@@ -863,9 +913,13 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.part_stat = nullptr;
   p.part_acc = nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p.c.d <= 64    ? fa::launch_attend<64>(p, workspace, s)
-                        : p.c.d <= 128 ? fa::launch_attend<128>(p, workspace, s)
-                                       : fa::launch_attend<256>(p, workspace, s);
+  auto launch = p.block_heads == 8 ? (p.c.d <= 64    ? fa::launch_attend<64, 1>
+                                      : p.c.d <= 128 ? fa::launch_attend<128, 1>
+                                                     : fa::launch_attend<256, 1>)
+                                   : (p.c.d <= 64    ? fa::launch_attend<64, 2>
+                                      : p.c.d <= 128 ? fa::launch_attend<128, 2>
+                                                     : fa::launch_attend<256, 2>);
+  const cudaError_t e = launch(p, workspace, s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
