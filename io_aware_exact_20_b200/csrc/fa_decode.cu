@@ -58,7 +58,8 @@ struct AttendParams {
   float scale_log2;  // softmax_scale * log2(e)
   int window, sinks;
   // partial results of the shares, null where no row can be cut
-  int2* cut_rows;         // [rows]: first and last share of each row
+  uint32_t grid;          // blocks, and the shares they can have at most
+  int shares;
   float2* part_stat;      // [2 * shares][16]: maximum (log2 units), row sum
   float* part_acc;        // [2 * shares][16][D]
 };
@@ -173,15 +174,32 @@ __device__ __forceinline__ void add_row8(float (&out)[8], float f, const float* 
   for (int e = 0; e < 8; ++e) out[e] = fmaf(f, v[e], out[e]);
 }
 
+// Beginning, ending and switching a row costs a warp about as much as a tile:
+// rows count as that much longer in the shares (64 ragged sequences of up to
+// 8192 keys 39 -> 30 us, the longest share no longer 13 us behind the median).
+constexpr int kRowCost = 2;
+
+// Tiles of sequence b's rows, 0 for a slot out of range or without keys, and
+// its slot and length.
+template <int KT>
+__device__ __forceinline__ int tiles_of(const AttendParams& p, int b, int* slot, int* len) {
+  *slot = p.slots != nullptr ? p.slots[b] : b;
+  *len = 0;
+  if (*slot >= 0 && *slot < p.c.slots)
+    *len = min(max(p.c.lengths[*slot], 0), p.c.max_pages * p.c.page_size);
+  return (visible_of(*len, p.window, p.sinks).count + KT - 1) / KT;
+}
+// What a row of that many tiles takes up in the shares.
+__device__ __forceinline__ uint32_t span_of(int tiles) { return tiles > 0 ? tiles + kRowCost : 0; }
+
 // The sequences that a block looks at together, in shared memory.
 struct Seqs {
   int len[kThreads], tiles[kThreads], slot[kThreads];
-  uint32_t upto[kThreads];  // running sum of tiles
+  uint32_t upto[kThreads];  // running sum of spans
   uint32_t scan[kWarps];
 };
 
-// A place in the walk: tile f of the row that spans [lo, hi) of the batch's
-// tiles, row rs (K / V head hk, block of heads) of sequence j of the chunk.
+// A place in the walk: tile f of the row that has tiles [lo, hi) of the batch's, row rs (K / V head hk, block of heads) of sequence j of the chunk.
 struct Cursor {
   uint32_t f, lo, hi;
   int j, rs, hk;
@@ -203,18 +221,13 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
 
   // ---- the shares: tiles of every sequence, their sum and this warp's part
-  auto load_seq = [&](int b) -> int {  // length and tiles of sequence b, this thread's
-    int n = 0, slot = -1;
-    if (b < p.batch) {
-      slot = p.slots != nullptr ? p.slots[b] : b;
-      if (slot >= 0 && slot < p.c.slots)
-        n = min(max(p.c.lengths[slot], 0), p.c.max_pages * p.c.page_size);
-    }
+  auto load_seq = [&](int b) -> uint32_t {  // sequence b, this thread's
+    int n = 0, slot = -1, tiles = 0;
+    if (b < p.batch) tiles = tiles_of<KT>(p, b, &slot, &n);
     sq.len[threadIdx.x] = n;
     sq.slot[threadIdx.x] = slot;
-    const int tiles = (visible_of(n, p.window, p.sinks).count + KT - 1) / KT;
     sq.tiles[threadIdx.x] = tiles;
-    return tiles;
+    return span_of(tiles);
   };
   // inclusive prefix sum over the block into sq.upto; returns the sum of all
   auto scan = [&](uint32_t x) -> uint32_t {
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
     __syncthreads();
     return all;
   };
-  uint32_t sum = 0, part = 0;  // tiles of one row per sequence
+  uint32_t sum = 0, part = 0;  // spans of one row per sequence
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     part = scan(load_seq(b0 + threadIdx.x));
     sum += part;
@@ -244,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   // (down to one tile each: shares of at least four took 10.8 us for one
   // sequence of 500 keys where these take 8.7, joining included)
   const uint32_t grid = gridDim.x;
-  const Shares sh(W, min(max(W, 1u), grid * kWarps));
+  const Shares sh(W, min(max(W, 1u), static_cast<uint32_t>(p.shares)));
   // few shares: one or two warps of a block, so that they spread over the SMs
   const uint32_t active = sh.n <= grid ? 1 : sh.n <= 2 * grid ? 2 : kWarps;
   const uint32_t blk0 = blockIdx.x * active;
@@ -275,9 +288,6 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
           if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
         }
-        if (p.cut_rows != nullptr)
-          for (int x = lane; x < rows_per_seq; x += 32)
-            p.cut_rows[static_cast<long long>(b) * rows_per_seq + x] = make_int2(0, 0);
       }
     }
     const uint32_t chunk_hi = chunk_lo + part * rows_per_seq;
@@ -295,12 +305,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           else a = mid + 1;
         }
         at.j = a;
-        const uint32_t tiles = sq.tiles[a];
-        const uint32_t seq_lo = chunk_lo + (sq.upto[a] - tiles) * rows_per_seq;
-        at.rs = (from - seq_lo) / tiles;
+        const uint32_t span = span_of(sq.tiles[a]);
+        const uint32_t seq_lo = chunk_lo + (sq.upto[a] - span) * rows_per_seq;
+        at.rs = (from - seq_lo) / span;
         at.hk = at.rs / p.head_blocks;
-        at.lo = seq_lo + at.rs * tiles;
-        at.hi = at.lo + tiles;
+        at.lo = seq_lo + at.rs * span;
+        at.hi = at.lo + sq.tiles[a];
         at.f = from;
       }
       // Where the block's four shares lie in one row its warps take turns, so that
@@ -311,19 +321,23 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
         end = blk_hi;
         step = kWarps;
       }
-      const uint32_t first = at.f;
       auto advance = [&](Cursor& c) {  // a tile on; c.f < end afterwards or the cursor is not used
         c.f += step;
         if (c.f < c.hi || c.f >= end) return;
+        c.lo = c.f = c.hi + kRowCost;
+        if (c.f >= end) return;
         if (++c.rs == rows_per_seq) {
           c.rs = 0;
           do ++c.j;
           while (sq.tiles[c.j] == 0);
         }
         c.hk = p.head_blocks == 1 ? c.rs : c.rs / p.head_blocks;
-        c.lo = c.hi;
-        c.hi += sq.tiles[c.j];
+        c.hi = c.lo + sq.tiles[c.j];
       };
+      if (at.f >= at.hi) {  // the share begins behind a row's last tile
+        at.f = at.hi - 1;
+        advance(at);
+      }
 
       // Page and row of this lane's key (lane & (KT - 1)) of the cursor's tile,
       // and the tile's K / V head.  The table cell is asked for a round before
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
       auto locate = [&](const Cursor& c) -> Key {
         Key r{-1, 0, c.hk};
         if (c.f >= end) return r;
-        if (c.f == c.lo || c.f == first) {
+        if (c.f == c.lo || c.f == at.f) {
           // a row begins: its Q into L2, a 128-byte line a lane
           const int hb = c.rs - c.hk * p.head_blocks, lines = (2 * p.c.d + 127) / 128;
           const int h = lane / lines;
@@ -415,14 +429,16 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
       Cursor fill = at;
       {
         Key ahead[STAGES - 1];
+        bool ahead_live[STAGES - 1];
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
+          ahead_live[s] = fill.f < end;
           ahead[s] = locate(fill);
           advance(fill);
         }
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
-          if (at.f + s * step < end) load(s, ahead[s]);
+          if (ahead_live[s]) load(s, ahead[s]);
           cp_async_commit();
         }
       }
@@ -445,10 +461,6 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
         const int hn = min(HB, p.group - hb * HB);  // its query heads
         const int b = b0 + at.j;
         if (begin) {
-          // the joining kernel learns the row's shares from the one it begins in
-          if (p.cut_rows != nullptr && at.lo >= lo && lane == 0)
-            p.cut_rows[static_cast<long long>(b) * rows_per_seq + at.rs] =
-                make_int2(share, at.hi <= hi ? share : sh.holding(at.hi - 1));
           // Q: zero past the row's heads and past d
           const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
 #pragma unroll
@@ -627,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
       }
       cp_async_wait<0>();
       if (block_row) {
-        // one partial result for the block, in its first share's place (the
-        // others' stay empty): a quarter of what the joining kernel would read
+        // one partial result for the block, in its first share's place: a quarter
+        // of what the joining kernel would read
         const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
         const int hn = min(HB, p.group - hb * HB);
         constexpr int LD = D + 4;  // (a warp's eight heads in different banks)
@@ -676,9 +688,6 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           a[1] = make_float4(out[4], out[5], out[6], out[7]);
           if (col == 0) {
             p.part_stat[row] = make_float2(mm, rs);
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w)
-              p.part_stat[2ll * (blk0 + w) * 16 + r] = make_float2(-INFINITY, 0.f);
           }
         }
         if (p.batch > kThreads) {
@@ -695,76 +704,113 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
 }
 
 // Joins the parts of rows that were cut: a block per (row, up to 4 of its query
-// heads).  First every part's weight 2^(m - M), all statistics at once, then
+// heads).  First the maximum and row sum of all parts' statistics at once, then
 // the weighted sums: D / 8 threads over a head's columns, the others over the
 // parts, whose loads wait for nothing (with the maximum carried from part to
-// part, 16 rows of 37 parts at d = 256 took 13 us).
+// part, 16 rows of 37 parts at d = 256 took 13 us).  Which rows were cut, and
+// where, follows from the lengths alone, so all of that happens before the wait
+// for the attention kernel (which starts its dependents only once the kernels
+// before it are done): small enough to be resident beside it, a block goes
+// on at once when it ends.
 constexpr int kJoinThreads = 256, kJoinHeads = 4;
-constexpr int kJoinParts = 148 * 4 * kWarps;  // a row has no more shares than a grid has warps
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
-  constexpr int TPR = D / 8, GROUPS = kJoinThreads / (TPR * kJoinHeads);
-  __shared__ float weight[kJoinHeads][kJoinParts];
-  __shared__ float2 red[kJoinThreads / 32][kJoinHeads];
+template <int D, int KT>
+__global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParams p) {
+  constexpr int TPR = D / 8, GROUPS = kJoinThreads / (TPR * kJoinHeads), kJoinWarps = kJoinThreads / 32;
+  __shared__ uint2 seqs[kJoinWarps];
+  __shared__ float2 red[kJoinWarps][kJoinHeads];
   __shared__ __align__(16) float acc[GROUPS][kJoinHeads][D];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int2 span = p.cut_rows[blockIdx.x];  // first and last share of the row
-  if (span.x >= span.y) return;              // written already
-  const int parts = span.y - span.x + 1;
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
   const int b = blockIdx.x / rows_per_seq, rs = blockIdx.x - b * rows_per_seq;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint2 sum = make_uint2(0u, 0u);  // spans of all sequences, and of those before b
+  for (int i = threadIdx.x; i < p.batch; i += kJoinThreads) {
+    int slot, len;
+    const uint32_t span = span_of(tiles_of<KT>(p, i, &slot, &len));
+    sum.x += span;
+    sum.y += i < b ? span : 0u;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+  }
+  if (lane == 0) seqs[warp] = sum;
+  int slot, len;
+  const int tiles = tiles_of<KT>(p, b, &slot, &len);
+  __syncthreads();
+  sum = make_uint2(0u, 0u);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    sum.x += seqs[w].x;
+    sum.y += seqs[w].y;
+  }
+  griddep_launch_dependents();
+  if (tiles == 0) return;
+  const uint32_t W = sum.x * rows_per_seq;
+  const Shares sh(W, min(max(W, 1u), static_cast<uint32_t>(p.shares)));
+  const uint32_t lo = sum.y * rows_per_seq + rs * span_of(tiles), hi = lo + tiles;
+  const uint32_t c0 = sh.holding(lo), c1 = sh.holding(hi - 1);
+  if (c0 == c1) return;  // written by the attention kernel
+  // The row's parts in order: shares c0 .. first - 1 one by one, from there to
+  // `last` the first share of every block that lies in the row, then one by one
+  // again to c1.
+  const uint32_t active = sh.n <= p.grid ? 1 : sh.n <= 2 * p.grid ? 2 : kWarps;
+  uint32_t first = (c0 + kWarps - 1) / kWarps * kWarps, last = c1 / kWarps * kWarps;
+  if (c0 % kWarps == 0 && lo != sh.begin(c0)) first += kWarps;
+  if ((c1 + 1) % kWarps == 0 && hi == sh.begin(c1 + 1)) last += kWarps;
+  if (active != kWarps || first >= last) first = last = c1 + 1;
+  const uint32_t n1 = first - c0, n2 = n1 + (last - first) / kWarps;
+  const uint32_t parts = n2 + c1 + 1 - last;
+  auto share_at = [&](uint32_t i) {
+    return i < n1 ? c0 + i : i < n2 ? first + (i - n1) * kWarps : last + (i - n2);
+  };
   const int hk = rs / p.head_blocks, hb = rs - hk * p.head_blocks;
   const int HB = p.block_heads;
   const int hn = min(HB, p.group - hb * HB) - blockIdx.y * kJoinHeads;  // this block's heads, and more
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // partial result i of head r of this block (see attend_kernel)
-  auto row_of = [&](int i, int r) {
-    return (2ll * (span.x + i) + (i == 0 ? 1 : 0)) * 16 + blockIdx.y * kJoinHeads + r;
+  // partial result of share c for head r of this block (see attend_kernel)
+  auto row_of = [&](uint32_t c, int r) {
+    return (2ll * c + (c == c0 ? 1 : 0)) * 16 + blockIdx.y * kJoinHeads + r;
   };
+  griddep_wait();
 
-  // weights: thread = (head threadIdx.x % 4, parts threadIdx.x / 4, + 64, ...);
-  // a part without keys, or merged into its block's first share, has sum 0
+  // statistics: thread = (head threadIdx.x % 4, parts threadIdx.x / 4, + 64, ...)
   const int hr = threadIdx.x % kJoinHeads;
-  float m = -INFINITY;
-  for (int i = threadIdx.x / kJoinHeads; i < parts; i += kJoinThreads / kJoinHeads) {
-    float x = -INFINITY;
-    if (hr < hn) {
-      const float2 st = p.part_stat[row_of(i, hr)];
-      if (st.y > 0.f) x = st.x;
+  float m = -INFINITY, l = 0.f;
+  if (hr < hn)
+    for (uint32_t i = threadIdx.x / kJoinHeads; i < parts; i += kJoinThreads / kJoinHeads) {
+      const float2 st = p.part_stat[row_of(share_at(i), hr)];
+      const float mm = fmaxf(m, st.x), ref = mm == -INFINITY ? 0.f : mm;
+      l = l * fast_exp2(m - ref) + st.y * fast_exp2(st.x - ref);
+      m = mm;
     }
-    weight[hr][i] = x;
-    m = fmaxf(m, x);
+#pragma unroll
+  for (int o = kJoinHeads; o < 32; o <<= 1) {  // in a fixed order
+    const float m1 = __shfl_xor_sync(0xffffffffu, m, o), l1 = __shfl_xor_sync(0xffffffffu, l, o);
+    const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
+    l = l * fast_exp2(m - ref) + l1 * fast_exp2(m1 - ref);
+    m = mm;
   }
-#pragma unroll
-  for (int o = kJoinHeads; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane < kJoinHeads) red[warp][lane].x = m;
+  if (lane < kJoinHeads) red[warp][lane] = make_float2(m, l);
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w][hr].x);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-  for (int i = threadIdx.x / kJoinHeads; i < parts; i += kJoinThreads / kJoinHeads) {
-    const float f = fast_exp2(weight[hr][i] - ref);
-    weight[hr][i] = f;
-    if (f > 0.f) sum += f * p.part_stat[row_of(i, hr)].y;
-  }
-  // (a fixed order of sums: lanes, then warps, then threads of a head below)
-#pragma unroll
-  for (int o = kJoinHeads; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane < kJoinHeads) red[warp][lane].y = sum;
-  __syncthreads();
-
   const int col = 8 * (threadIdx.x % TPR), x = threadIdx.x / TPR;
   const int r = x % kJoinHeads, group = x / kJoinHeads;
+  m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[w][r].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) l += red[w][r].y * fast_exp2(red[w][r].x - ref);
   float out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.f;
   if (r < hn) {
-#pragma unroll 8
-    for (int i = group; i < parts; i += GROUPS)
-      if (weight[r][i] > 0.f) add_row8(out, weight[r][i], p.part_acc + row_of(i, r) * D + col);
+#pragma unroll 4
+    for (uint32_t i = group; i < parts; i += GROUPS) {
+      const long long row = row_of(share_at(i), r);
+      add_row8(out, fast_exp2(p.part_stat[row].x - ref), p.part_acc + row * D + col);
+    }
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[group][r][col + e] = out[e];
@@ -772,13 +818,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
   if (group != 0 || col >= p.c.d || r >= hn) return;
 #pragma unroll
   for (int w = 1; w < GROUPS; ++w) add_row8(out, 1.f, &acc[w][r][col]);
-  float mm = -INFINITY, all = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    mm = fmaxf(mm, red[w][r].x);
-    all += red[w][r].y;
-  }
-  write_row(p, b, hk * p.group + hb * HB + blockIdx.y * kJoinHeads + r, col, mm, all, out);
+  write_row(p, b, hk * p.group + hb * HB + blockIdx.y * kJoinHeads + r, col, m, l, out);
 }
 
 // Grid and workspace of a call, from what the host knows: the longest that a
@@ -789,7 +829,7 @@ struct Plan {
   long long tiles;  // at most, of the whole batch
   long long grid;
   bool cut;
-  size_t off_stat, off_acc, bytes;
+  size_t off_acc, bytes;
 };
 
 template <int NB>
@@ -814,12 +854,11 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const long long tiles = (most + KT - 1) / KT;
   const long long rows = static_cast<long long>(batch) * c.heads_kv * ((G + HB - 1) / HB);
   Plan p;
-  p.tiles = rows * tiles;
+  p.tiles = rows * (tiles + kRowCost);
   p.grid = p.tiles < 148ll * per_sm ? p.tiles : 148ll * per_sm;
   p.cut = tiles > 1;
-  p.off_stat = (static_cast<size_t>(rows) * sizeof(int2) + 255) / 256 * 256;
   const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
-  p.off_acc = p.off_stat + parts * sizeof(float2);
+  p.off_acc = parts * sizeof(float2);
   p.bytes = p.cut ? p.off_acc + parts * D * sizeof(float) : 0;
   return p;
 }
@@ -837,16 +876,17 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
   if (e != cudaSuccess) return e;
   const Plan plan = plan_of(p.c, p.batch, p.heads, p.window, p.sinks);
   AttendParams a = p;
+  a.grid = static_cast<uint32_t>(plan.grid);
+  a.shares = static_cast<int>(plan.grid) * kWarps;
   if (plan.cut) {
     char* ws = static_cast<char*>(workspace);
-    a.cut_rows = reinterpret_cast<int2*>(ws);
-    a.part_stat = reinterpret_cast<float2*>(ws + plan.off_stat);
+    a.part_stat = reinterpret_cast<float2*>(ws);
     a.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
   }
   cudaError_t r = launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), dim3(kThreads), C::SMEM,
                                     stream, a);
   if (r == cudaSuccess && plan.cut)
-    r = launch_overlapped(join_kernel<D>,
+    r = launch_overlapped(join_kernel<D, C::KT>,
                           dim3(static_cast<unsigned>(p.batch * p.c.heads_kv * p.head_blocks),
                                static_cast<unsigned>(((p.group < p.block_heads ? p.group : p.block_heads) + kJoinHeads - 1) / kJoinHeads)),
                           dim3(kJoinThreads), 0, stream, a);
@@ -909,7 +949,6 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * fa::kLog2e);
   p.window = window;
   p.sinks = sinks;
-  p.cut_rows = nullptr;
   p.part_stat = nullptr;
   p.part_acc = nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
