@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
 // moves: a warp per (move, layer, K or V, head)
 // ---------------------------------------------------------------------------
 
+constexpr int kAhead = 8;
+
 __global__ void __launch_bounds__(256) move_kernel(const Cache from, const Cache to, const Moves m) {
   griddep_wait();
   griddep_launch_dependents();
@@ -217,10 +219,21 @@ __global__ void __launch_bounds__(256) move_kernel(const Cache from, const Cache
                          (is_v ? layer * to.v_layer + m.dst[i] * to.v_page + h * to.v_head
                                : layer * to.k_layer + m.dst[i] * to.k_page + h * to.k_head);
     const long long src_row = is_v ? from.v_row : from.k_row, dst_row = is_v ? to.v_row : to.k_row;
-    for (int x = lane; x < rows * chunks; x += 32) {
-      const int row = x / chunks, col = 8 * (x - row * chunks);
-      *reinterpret_cast<uint4*>(dst + row * dst_row + col) =
-          *reinterpret_cast<const uint4*>(src + row * src_row + col);
+    // eight loads in flight a lane, then their stores (697 MB read and written:
+    // 116 us, 6.0 TB/s; with each load followed by its store 124)
+    const int total = rows * chunks;
+    for (int x0 = lane; x0 < total; x0 += 32 * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int x = x0 + 32 * u, row = x / chunks, col = 8 * (x - row * chunks);
+        if (x < total) v[u] = *reinterpret_cast<const uint4*>(src + row * src_row + col);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int x = x0 + 32 * u, row = x / chunks, col = 8 * (x - row * chunks);
+        if (x < total) *reinterpret_cast<uint4*>(dst + row * dst_row + col) = v[u];
+      }
     }
   }
 }
@@ -268,18 +281,29 @@ __global__ void __launch_bounds__(256) write_kernel(const WriteParams p) {
   if (page < 0 || page >= p.c.pages) return;
   const int row = static_cast<int>(pos - cell * p.c.page_size);
   const int chunks = p.c.d / 8, half = p.c.heads_kv * chunks;
-  for (int x = lane; x < 2 * half; x += 32) {
-    const bool is_v = x >= half;
-    const int y = is_v ? x - half : x;
-    const int h = y / chunks, col = 8 * (y - h * chunks);
-    const __nv_bfloat16* src = is_v ? p.v + t * p.v_row + h * p.v_head + col
-                                    : p.k + t * p.k_row + h * p.k_head + col;
-    __nv_bfloat16* dst =
-        is_v ? static_cast<__nv_bfloat16*>(p.c.v) + p.layer * p.c.v_layer + page * p.c.v_page +
-                   h * p.c.v_head + row * p.c.v_row + col
-             : static_cast<__nv_bfloat16*>(p.c.k) + p.layer * p.c.k_layer + page * p.c.k_page +
-                   h * p.c.k_head + row * p.c.k_row + col;
-    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+  const __nv_bfloat16 *ks = p.k + t * p.k_row, *vs = p.v + t * p.v_row;
+  __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.c.k) + p.layer * p.c.k_layer +
+                      page * p.c.k_page + row * p.c.k_row;
+  __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.c.v) + p.layer * p.c.v_layer +
+                      page * p.c.v_page + row * p.c.v_row;
+  constexpr int kPieces = 4;  // loads in flight a lane, as in move_kernel
+  for (int x0 = lane; x0 < 2 * half; x0 += 32 * kPieces) {
+    uint4 v[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int x = x0 + 32 * u, y = x >= half ? x - half : x;
+      const int h = y / chunks, col = 8 * (y - h * chunks);
+      if (x < 2 * half)
+        v[u] = *reinterpret_cast<const uint4*>(x >= half ? vs + h * p.v_head + col
+                                                         : ks + h * p.k_head + col);
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int x = x0 + 32 * u, y = x >= half ? x - half : x;
+      const int h = y / chunks, col = 8 * (y - h * chunks);
+      if (x < 2 * half)
+        *reinterpret_cast<uint4*>(x >= half ? vd + h * p.c.v_head + col : kd + h * p.c.k_head + col) = v[u];
+    }
   }
 }
 
@@ -362,20 +386,32 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Cache 
   griddep_launch_dependents();
   const int tid = threadIdx.x;
   int mine = 0;
+#pragma unroll 8
   for (int p = tid; p < c.pages; p += kPlanThreads) mine += c.refs[p] > 0;
   int count = 0;
   block_scan(mine, scan, &count);
-  // the k-th free page below `count` receives the k-th used one from it on
+  // the k-th free page below `count` receives the k-th used one from it on;
+  // eight consecutive pages a thread and scan
+  constexpr int kPer = 8;
   int holes = 0, movers = 0;
-  for (int p0 = 0; p0 < c.pages; p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    const bool in_use = p < c.pages && c.refs[p] > 0;
-    const bool hole = p < count && !in_use, mover = p >= count && in_use;
+  for (int p0 = 0; p0 < c.pages; p0 += kPer * kPlanThreads) {
+    const int p = p0 + kPer * tid;
+    uint32_t used_bits = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (p + u < c.pages && c.refs[p + u] > 0) used_bits |= 1u << u;
+    const uint32_t below = low_bits(min(kPer, count - p)), inside = low_bits(min(kPer, c.pages - p));
+    const uint32_t hole_bits = below & inside & ~used_bits, mover_bits = ~below & used_bits;
     int total = 0;
-    const int at = block_scan(hole ? 1 : mover ? 1 << 16 : 0, scan, &total);
-    if (hole) w.moves.dst[holes + (at & 0xFFFF) - 1] = p;
-    if (mover) w.moves.src[movers + (at >> 16) - 1] = p;
-    if (!mover && p >= count && p < c.pages) w.now[p] = p;
+    const int own = __popc(hole_bits) | __popc(mover_bits) << 16;
+    const int at = block_scan(own, scan, &total) - own;
+    int hole = holes + (at & 0xFFFF), mover = movers + (at >> 16);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      if ((hole_bits >> u) & 1u) w.moves.dst[hole++] = p + u;
+      if ((mover_bits >> u) & 1u) w.moves.src[mover++] = p + u;
+      else if (p + u >= count && p + u < c.pages) w.now[p + u] = p + u;
+    }
     holes += total & 0xFFFF;
     movers += total >> 16;
   }

@@ -746,6 +746,9 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
     sum.y += seqs[w].y;
   }
   griddep_launch_dependents();
+  // one block waits whatever its row: this grid must not be done before the
+  // attention kernel is, or a kernel behind it could start beside that one
+  if (blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
   if (tiles == 0) return;
   const uint32_t W = sum.x * rows_per_seq;
   const Shares sh(W, min(max(W, 1u), static_cast<uint32_t>(p.shares)));
@@ -926,7 +929,7 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   if (batch == 0) return FA_OK;
   if (!fa::cache_aligned(q, 16) || !fa::cache_aligned(o, 16) || !fa::cache_aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(batch) * heads > 0x7FFFFFFF) return FA_ERR_UNSUPPORTED;
+  if (heads > 65535 || static_cast<int64_t>(batch) * heads > 0x7FFFFFFF) return FA_ERR_UNSUPPORTED;
   const fa::Plan plan = fa::plan_of(p.c, batch, heads, window, sinks);
   if (plan.tiles > 0xFFFFFFFFll - 65536) return FA_ERR_UNSUPPORTED;  // 32-bit counts in the kernels
   const size_t need = plan.bytes;

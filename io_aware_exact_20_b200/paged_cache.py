@@ -73,14 +73,11 @@ class PagedCache:
             raise ValueError(f"{name}: {n} entries are expected, got {t.shape[0]}")
         return t.data_ptr()
 
-    def _empty(self, shape, dtype):
-        return self._torch.empty(shape, dtype=dtype, device=self.device)
-
     def _workspace(self, n):
         size = self._sizes.get(n)
         if size is None:  # a function of the cache's sizes and n alone
             size = self._sizes[n] = self._lib.fa_cache_workspace_size(self._ref, n)
-        return self._empty(size, self._torch.uint8), size
+        return self.lengths.new_empty(size // 4), size
 
     def _call(self, fn, *args):
         """The C call on the cache's device and that device's current stream."""
@@ -98,7 +95,7 @@ class PagedCache:
         """Grows slots[i] by tokens[i]; returns start (int32 [n]), each entry's
         first new position, -1 where it was not granted (fa_cache_extend)."""
         n = slots.shape[0]
-        start = self._empty(n, self._torch.int32)
+        start = self.lengths.new_empty(n)
         ws, size = self._workspace(n)
         self._call(self._lib.fa_cache_extend, self._ints("slots", slots, n),
                    self._ints("tokens", tokens, n), n, start.data_ptr(), ws.data_ptr(), size)
@@ -138,10 +135,10 @@ class PagedCache:
         if H < 1 or H % self.heads_kv:
             raise ValueError("q's heads must be a multiple of the cache's")
         if out is None:
-            out = self._empty(shape, torch.bfloat16)
+            out = q.new_empty(shape)
         so = out.stride()
         if lse is None:
-            lse = self._empty((B, H), torch.float32)
+            lse = q.new_empty((B, H), dtype=torch.float32)
         elif (lse.shape != (B, H) or lse.dtype is not torch.float32 or lse.get_device() != self._index
               or not lse.is_contiguous()):
             raise ValueError(f"lse: contiguous float32 {(B, H)} on the cache's device is expected")
@@ -155,7 +152,7 @@ class PagedCache:
         size = self._sizes.get(key)
         if size is None:  # a function of the cache's sizes and these alone
             size = self._sizes[key] = self._lib.fa_cache_attend_workspace_size(self._ref, *key)
-        ws = self._empty(size, torch.uint8) if size else None
+        ws = self.lengths.new_empty((size + 3) // 4) if size else None
         self._call(self._lib.fa_cache_attend, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
                    sq[0], sq[1], so[0], so[1],
                    None if slots is None else self._ints("slots", slots, B), B, H,
@@ -181,7 +178,7 @@ class PagedCache:
     def compact(self):
         """Moves the pages in use into the lowest numbers; returns how many there
         are (int32 [1], on the device)."""
-        used = self._empty(1, self._torch.int32)
+        used = self.lengths.new_empty(1)
         ws, size = self._workspace(0)
         self._call(self._lib.fa_cache_compact, used.data_ptr(), ws.data_ptr(), size)
         return used

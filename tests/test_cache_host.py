@@ -114,7 +114,7 @@ def test_bad_writes_are_refused(lib, change, code):
     (dict(heads=0), 1), (dict(scale=0.0), 1), (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1),
     (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(q_head=4), 1), (dict(o_head=0), 1), (dict(o_batch=0), 1),
     (dict(slots=A16 + 2), 1), (dict(batch=-1), 1), (dict(batch=0), 0),
-    (dict(batch=(1 << 30), heads=2), 2),
+    (dict(batch=(1 << 30), heads=2), 2), (dict(heads=65536), 2),
 ])
 def test_bad_attends_are_refused(lib, change, code):
     a = dict(layer=0, q=A16, o=A16, lse=A16, q_batch=256, q_head=64, o_batch=256, o_head=64, slots=None, batch=2,

@@ -451,3 +451,39 @@ def test_empty_calls(lib):
     assert o.shape == (0, 4, 32) and lse.shape == (0, 4)
     assert cache.compact().tolist() == [0]
     model.check(cache)
+
+
+@pytest.mark.parametrize("B,P,H,Hkv,d,window,sinks", [
+    (300, 16, 8, 2, 96, 0, 0), (130, 8, 20, 1, 64, 50, 3), (257, 4, 2, 2, 256, 0, 0), (1000, 16, 4, 1, 128, 0, 0)])
+def test_attend_many_sequences(lib, B, P, H, Hkv, d, window, sinks):
+    """More sequences than a block looks at together: short, empty and one long one among them."""
+    r = random.Random(B)
+    lens = [r.choice([0, 1, 5, 16, 17, r.randrange(60)]) for _ in range(B)]
+    lens[B // 2] = 9000
+    cache = filled(lib, lens, P, Hkv, d, seed=B)
+    q = randn((B, H, d), 64)
+    slots = list(range(B))
+    r.shuffle(slots)
+    o, lse = cache.attend(0, q, ints(slots), window=window, sinks=sinks)
+    some = sorted(set([0, 127 % B, 128 % B, B - 1, slots.index(B // 2)] + [r.randrange(B) for _ in range(25)]))
+    check_attend(cache, 0, q[some], [slots[i] for i in some], o[some], lse[some], d ** -0.5, window, sinks)
+    empty = [i for i in range(B) if lens[slots[i]] == 0]
+    assert (o[empty] == 0).all() and (lse[empty] == float("-inf")).all()
+
+
+def test_attend_leads_to_the_next_call_in_order(lib):
+    """Rows that need no joining: the joining kernel has nothing to wait for, yet
+    a write behind it must not reach the pages while they are read."""
+    cache = filled(lib, [16] * 2000, 16, 1, 128, seed=21)
+    q, start = randn((2000, 1, 128), 65), ints([0] * 2000)
+    slots = ints(list(range(2000)))
+    want = cache.attend(0, q, slots)
+    junk = torch.full((2000, 1, 128), 1e4, dtype=torch.bfloat16, device="cuda")
+    keep = cache.k.clone(), cache.v.clone()
+    for _ in range(20):
+        got = cache.attend(0, q, slots)
+        cache.write(0, junk, junk, slots, start)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        cache.k.copy_(keep[0])
+        cache.v.copy_(keep[1])

@@ -1,0 +1,34 @@
+"""The windowed attention's tests under the bounds-checking build of the library
+(every access outside TMA checked against its buffer), and the cache calls'
+refusals under AddressSanitizer and UndefinedBehaviorSanitizer."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+
+from test_host_sanitizers import _env, _runtime
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.mark.gpu
+def test_window_suite_under_the_bounds_checking_build(lib):
+    from io_aware_exact_20_b200 import build
+    env = dict(os.environ, FA_B200_LIBRARY=build.build_variant("bounds"))
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_window.py", "-m", "gpu", "-q", "-x",
+                        "-p", "no:cacheprovider"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
+
+
+def test_cache_refusals_under_asan_and_ubsan(lib):
+    if _runtime("libasan.so") is None or _runtime("libubsan.so") is None:
+        pytest.skip("the gcc sanitizer runtimes are not installed")
+    from io_aware_exact_20_b200 import build
+    env = _env(build.build_variant("sanitize"))
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_cache_host.py", "tests/test_window_host.py", "-q",
+                        "-p", "no:cacheprovider"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    report = r.stdout[-3000:] + r.stderr[-3000:]
+    assert r.returncode == 0, report
+    assert "AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr, report
