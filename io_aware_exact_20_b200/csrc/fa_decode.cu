@@ -24,6 +24,12 @@
 // (fp32 sums with their maximum and row sum) and joined, in the order of the
 // shares, by a second kernel; other rows are written at once.
 //
+// Few rows of few tiles, where latency counts, take another way to the same sums:
+// a cluster of up to 8 blocks per row, whose warps take turns, and whose parts
+// meet through the cluster's shared memory: one launch, no shares to work out
+// and nothing to join (one sequence of 500 keys 6.8 us instead of 9.5, 64 of 60 keys 5.6
+// instead of 11.2).
+//
 // Visible keys are counted u = 0 .. n_vis - 1: the first `sinks` that the window
 // does not reach, then the window.  A tile is KT consecutive u, each with its
 // own table lookup, so pages may be of any size, tiles may straddle pages, and
@@ -58,6 +64,7 @@ struct AttendParams {
   float scale_log2;  // softmax_scale * log2(e)
   int window, sinks;
   // partial results of the shares, null where no row can be cut
+  int cluster;            // blocks per row (CL)
   uint32_t grid;          // blocks, and the shares they can have at most
   int shares;
   float2* part_stat;      // [2 * shares][16]: maximum (log2 units), row sum
@@ -111,6 +118,20 @@ __device__ __forceinline__ float sum_rows(float x) {
 // Asks for a line that will be read soon.
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// All threads of the cluster's blocks meet; what they wrote to shared memory
+// before is seen by all of them after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Two floats from the same place in the shared memory of the cluster's block c.
+__device__ __forceinline__ float2 cluster_load2(const void* p, uint32_t c) {
+  uint32_t at;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(c));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
 }
 
 constexpr int kWarps = 4;
@@ -205,7 +226,8 @@ struct Cursor {
   int j, rs, hk;
 };
 
-template <int D, int NB>
+// CL: a cluster per row (see the head of the file).
+template <int D, int NB, bool CL>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
     attend_kernel(const AttendParams p) {
   using C = DecodeCfg<D, NB>;
@@ -248,6 +270,464 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
     __syncthreads();
     return all;
   };
+  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
+  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
+
+  if (p.c.d < D)
+    for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
+  __syncwarp();
+
+  uint32_t lo = 0, blk_lo = 0, blk_hi = 0, blk0 = 0, share = 0;  // of the shares, below
+  // The tiles of one warp: from `at` to `end` in steps of `step`, through the rows
+  // of the sequences that begin at b0.  block_row: all of the block's warps work
+  // on this one row, and their parts meet at the end.
+  auto walk = [&](int b0, Cursor at, uint32_t end, uint32_t step, bool block_row) {
+    auto advance = [&](Cursor& c) {  // a tile on; c.f < end afterwards or the cursor is not used
+      c.f += step;
+      if (c.f < c.hi || c.f >= end) return;
+      c.lo = c.f = c.hi + kRowCost;
+      if (c.f >= end) return;
+      if (++c.rs == rows_per_seq) {
+        c.rs = 0;
+        do ++c.j;
+        while (sq.tiles[c.j] == 0);
+      }
+      c.hk = p.head_blocks == 1 ? c.rs : c.rs / p.head_blocks;
+      c.hi = c.lo + sq.tiles[c.j];
+    };
+    if (!CL && at.f >= at.hi) {  // the share begins behind a row's last tile
+      at.f = at.hi - 1;
+      advance(at);
+    }
+
+    // Page and row of this lane's key (lane & (KT - 1)) of the cursor's tile,
+    // and the tile's K / V head.  The table cell is asked for a round before
+    // copies need it, and nothing is computed from it until then.
+    struct Key {
+      int page, row, hk;
+    };
+    auto locate = [&](const Cursor& c) -> Key {
+      Key r{-1, 0, c.hk};
+      if (c.f >= end) return r;
+      if (c.f == c.lo || c.f == at.f) {
+        // a row begins: its Q into L2, a 128-byte line a lane
+        const int hb = c.rs - c.hk * p.head_blocks, lines = (2 * p.c.d + 127) / 128;
+        const int h = lane / lines;
+        if (h < min(HB, p.group - hb * HB))
+          prefetch_l2(p.q + (b0 + c.j) * p.q_batch + (c.hk * p.group + hb * HB + h) * p.q_head +
+                      (lane - h * lines) * 64);
+      }
+      const Visible vis = visible_of(sq.len[c.j], p.window, p.sinks);
+      const int u = static_cast<int>(c.f - c.lo) * KT + (lane & (KT - 1));
+      if (u < vis.count) {
+        const int j = vis.key(u);
+        const int cell = j / p.c.page_size;
+        r.row = j - cell * p.c.page_size;
+        r.page = p.c.table[static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell];
+      }
+      return r;
+    };
+    // copies of one tile into a stage: whole rows, 16 bytes a lane
+    auto load = [&](int stage, const Key& r) {
+      constexpr int CH = D / 8, RPI = 32 / CH;  // pieces of a row, rows per step
+      const int c = lane % CH;
+      const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
+      const uint32_t live = __ballot_sync(0xffffffffu, r.page >= 0 && r.page < p.c.pages);
+      if (lane == 0) valid[stage] = live;
+      const bool col_ok = 8 * c < p.c.d;  // past d the ring holds zeros
+      const __nv_bfloat16* kh = p.k + r.hk * p.c.k_head + 8 * c;
+      const __nv_bfloat16* vh = p.v + r.hk * p.c.v_head + 8 * c;
+      // Most tiles are one run of consecutive rows, or two (where the tile crosses
+      // a page, or from the first tokens into the window): one or two places to
+      // start from instead of one per row.  (With two places for every tile, d =
+      // 256 took 119 us where it takes 93.)
+      const int x = lane & (KT - 1);
+      const int page0 = __shfl_sync(0xffffffffu, r.page, 0), row0 = __shfl_sync(0xffffffffu, r.row, 0);
+      const uint32_t other = __ballot_sync(0xffffffffu, r.page != page0 || r.row != row0 + x);
+      const bool all_live = live == 0xffffffffu;
+      const int row_l = lane / CH;
+      const __nv_bfloat16* k0 = kh + page0 * p.c.k_page + (row0 + row_l) * p.c.k_row;
+      const __nv_bfloat16* v0 = vh + page0 * p.c.v_page + (row0 + row_l) * p.c.v_row;
+      if (all_live && other == 0u) {
+#pragma unroll
+        for (int s = 0; s < KT / RPI; ++s) {
+          const int row = s * RPI + row_l;
+          const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+          if (!col_ok) break;
+          cp_async16(kdst + dst, k0 + s * RPI * p.c.k_row, true);
+          cp_async16(vdst + dst, v0 + s * RPI * p.c.v_row, true);
+        }
+        return;
+      }
+      const int cut = other ? __ffs(other) - 1 : 0;  // first row of the second run
+      const int page1 = __shfl_sync(0xffffffffu, r.page, cut);
+      const int row1 = __shfl_sync(0xffffffffu, r.row, cut) - cut;
+      if (__all_sync(0xffffffffu, all_live && (x < cut || (r.page == page1 && r.row == row1 + x)))) {
+        const __nv_bfloat16* k1 = kh + page1 * p.c.k_page + (row1 + row_l) * p.c.k_row;
+        const __nv_bfloat16* v1 = vh + page1 * p.c.v_page + (row1 + row_l) * p.c.v_row;
+#pragma unroll
+        for (int s = 0; s < KT / RPI; ++s) {
+          const int row = s * RPI + row_l;
+          const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+          if (!col_ok) break;
+          cp_async16(kdst + dst, (row < cut ? k0 : k1) + s * RPI * p.c.k_row, true);
+          cp_async16(vdst + dst, (row < cut ? v0 : v1) + s * RPI * p.c.v_row, true);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < KT / RPI; ++s) {
+          const int row = s * RPI + lane / CH;
+          const int page = __shfl_sync(0xffffffffu, r.page, row), at_row = __shfl_sync(0xffffffffu, r.row, row);
+          const bool ok = (live >> row) & 1u;
+          const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
+          if (!col_ok) continue;
+          cp_async16(kdst + dst, ok ? kh + page * p.c.k_page + at_row * p.c.k_row : p.k, ok);
+          cp_async16(vdst + dst, ok ? vh + page * p.c.v_page + at_row * p.c.v_row : p.v, ok);
+        }
+      }
+    };
+
+    Cursor fill = at;
+    {
+      Key ahead[STAGES - 1];
+      bool ahead_live[STAGES - 1];
+#pragma unroll
+      for (int s = 0; s < STAGES - 1; ++s) {
+        ahead_live[s] = fill.f < end;
+        ahead[s] = locate(fill);
+        advance(fill);
+      }
+#pragma unroll
+      for (int s = 0; s < STAGES - 1; ++s) {
+        if (ahead_live[s]) load(s, ahead[s]);
+        cp_async_commit();
+      }
+    }
+    Key next = locate(fill);
+
+    uint32_t qb[NB][D / 16][2];  // Q as the B operand: column g is a head
+    float o[NB][D / 16][4];      // O^T: rows g, g + 8 of 16 columns of V; heads 2 q4, 2 q4 + 1
+    float m[NB][2], l[NB][2];    // of those heads; l: this lane's keys alone
+    bool begin = true;
+    int stage = 0;
+    if constexpr (CL) {  // a warp without tiles takes part in the meeting all the same
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[nb][i][u] = 0.f;
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.f;
+      }
+    }
+    while (at.f < end) {
+      // the next free stage was read in the previous round
+      __syncwarp();
+      if (fill.f < end) load(stage == 0 ? STAGES - 1 : stage - 1, next);
+      cp_async_commit();
+      advance(fill);
+      next = locate(fill);
+      const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
+      const int h0 = hk * p.group + hb * HB;      // first query head of the row
+      const int hn = min(HB, p.group - hb * HB);  // its query heads
+      const int b = b0 + at.j;
+      if (begin) {
+        // Q: zero past the row's heads and past d
+        const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int h = 8 * nb + g;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int col = 16 * kk + 8 * u + 2 * q4;
+              qb[nb][kk][u] = h < hn && col < p.c.d
+                                  ? *reinterpret_cast<const uint32_t*>(q0 + h * p.q_head + col)
+                                  : 0u;
+            }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[nb][i][u] = 0.f;
+          m[nb][0] = m[nb][1] = -INFINITY;
+          l[nb][0] = l[nb][1] = 0.f;
+        }
+        begin = false;
+      }
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      const uint32_t kbase = ring + stage * C::STAGE, vbase = kbase + KT * C::ROW;
+      const uint32_t live = valid[stage];
+      constexpr int MT = KT / 16;  // 16-key rows of S^T
+      // two sums per score, over the even and the odd steps: half the chain
+      float s[MT][NB][4], s1[MT][NB][4];
+#pragma unroll
+      for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[kt][nb][u] = s1[kt][nb][u] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int kt = 0; kt < MT; ++kt) {
+          uint32_t ka[4];
+          const int row = kt * 16 + (lane & 15), ch = 2 * kk + (lane >> 4);
+          ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), ka);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816(kk & 1 ? s1[kt][nb] : s[kt][nb], ka, qb[nb][kk][0], qb[nb][kk][1]);
+        }
+#pragma unroll
+      for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[kt][nb][u] += s1[kt][nb][u];
+      constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
+      if ((live & kAll) != kAll) {
+#pragma unroll
+        for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              s[kt][nb][u] = (live >> (16 * kt + g + 8 * (u >> 1))) & 1u ? s[kt][nb][u] : -INFINITY;
+      }
+      // Online softmax over the tile's keys, per head of this lane's pair; P is
+      // rounded to bf16 for the second product, as in the other attention
+      // kernels, and turned from rows of keys to columns (the B operand); the
+      // row sum keeps the unrounded values
+      uint32_t pb[NB][MT][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float alpha[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int kt = 0; kt < MT; ++kt) mx = fmax3(mx, s[kt][nb][u], s[kt][nb][u + 2]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          const float m_new = fmaxf(m[nb][u], mx * p.scale_log2);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          alpha[u] = fast_exp2(m[nb][u] - ref);
+          m[nb][u] = m_new;
+          float sum = 0.f;
+#pragma unroll
+          for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float e = fast_exp2(fmaf(s[kt][nb][u + 2 * r], p.scale_log2, -ref));
+              s[kt][nb][u + 2 * r] = e;
+              sum += e;
+            }
+          l[nb][u] = l[nb][u] * alpha[u] + sum;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[nb][i][u] *= alpha[u & 1];
+        }
+#pragma unroll
+        for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            pb[nb][kt][r] = transpose8x8(pack_bf16(s[kt][nb][2 * r], s[kt][nb][2 * r + 1]));
+      }
+#pragma unroll
+      for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+        for (int dd = 0; dd < D / 16; ++dd) {
+          uint32_t va[4];
+          const int row = kt * 16 + (lane & 7) + (lane >> 4) * 8, ch = 2 * dd + ((lane >> 3) & 1);
+          ldsm_x4_trans(vbase + row * C::ROW + ((ch ^ (row & 7)) << 4), va);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][dd], va, pb[nb][kt][0], pb[nb][kt][1]);
+        }
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+
+      const uint32_t f1 = at.f + 1;
+      if (block_row) {
+        if (at.f + step < end) {
+          advance(at);
+          continue;
+        }
+        break;  // the warps' parts of this row meet below
+      } else if (f1 == at.hi || f1 == end) {
+        // the row ends, or the share: the whole row goes to O and LSE, a part of
+        // it to the share's partial results, index 1 where the row begins in
+        // this share, 0 where it goes on
+        const bool begins = at.lo >= lo, whole = begins && f1 == at.hi;
+        const long long pr = (2ll * share + (begins ? 1 : 0)) * 16;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float inv[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            l[nb][u] = sum_rows(l[nb][u]);
+            inv[u] = l[nb][u] > 0.f ? 1.f / l[nb][u] : 0.f;
+            const int h = 8 * nb + 2 * q4 + u;
+            if (g == 0 && h < hn) {
+              if (whole)
+                p.lse[static_cast<long long>(b) * p.heads + h0 + h] =
+                    l[nb][u] > 0.f ? (m[nb][u] + log2f(l[nb][u])) * kLn2 : -INFINITY;
+              else
+                p.part_stat[pr + h] = make_float2(m[nb][u], l[nb][u]);
+            }
+          }
+          if (whole) {
+            // pairs of columns of V for head g, out of pairs of heads
+            __nv_bfloat16* dst = p.o + b * p.o_batch + (h0 + 8 * nb + g) * p.o_head + 2 * q4;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t x =
+                    transpose8x8(pack_bf16(o[nb][i][2 * r] * inv[0], o[nb][i][2 * r + 1] * inv[1]));
+                const int col = 16 * i + 8 * r;
+                if (8 * nb + g < hn && col < p.c.d) *reinterpret_cast<uint32_t*>(dst + col) = x;
+              }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int h = 8 * nb + 2 * q4 + u;
+              float* dst = p.part_acc + (pr + h) * D + g;
+              if (h < hn)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  dst[16 * i] = o[nb][i][u];
+                  dst[16 * i + 8] = o[nb][i][2 + u];
+                }
+            }
+          }
+        }
+        begin = true;
+      }
+      advance(at);
+    }
+    cp_async_wait<0>();
+    if (block_row) {
+      // one partial result for the block, in its first share's place: a quarter
+      // of what the joining kernel would read
+      const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
+      const int hn = min(HB, p.group - hb * HB);
+      constexpr int LD = D + 4;  // (a warp's eight heads in different banks)
+      __syncthreads();
+      float2* stat = reinterpret_cast<float2*>(smem);  // [warp][HB], then [warp][HB][LD] sums
+      float* acc = reinterpret_cast<float*>(smem + kWarps * HB * sizeof(float2));
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int h = warp * HB + 8 * nb + 2 * q4 + u;
+          const float sum = sum_rows(l[nb][u]);
+          if (g == 0) stat[h] = make_float2(m[nb][u], sum);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[h * LD + 16 * i + g] = o[nb][i][u];
+            acc[h * LD + 16 * i + 8 + g] = o[nb][i][2 + u];
+          }
+        }
+      float2* stat2 = reinterpret_cast<float2*>(acc + kWarps * HB * LD);  // CL: [HB], then [HB][D]
+      float* acc2 = reinterpret_cast<float*>(stat2 + HB);
+      __syncthreads();
+      const bool begins = at.lo >= blk_lo, whole = begins && at.hi == blk_hi;
+      for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
+        const int r = x / (D / 8), col = 8 * (x % (D / 8));
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * HB + r].x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float rs = 0.f, out[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 st = stat[w * HB + r];
+          const float f = fast_exp2(st.x - ref);
+          rs += f * st.y;
+          add_row8(out, f, acc + (w * HB + r) * LD + col);
+        }
+        if constexpr (CL) {  // to the cluster: sums and statistics of this block
+          float4* a = reinterpret_cast<float4*>(acc2 + r * D + col);
+          a[0] = make_float4(out[0], out[1], out[2], out[3]);
+          a[1] = make_float4(out[4], out[5], out[6], out[7]);
+          if (col == 0) stat2[r] = make_float2(mm, rs);
+          continue;
+        }
+        if (whole) {
+          if (col < p.c.d) write_row(p, b0 + at.j, hk * p.group + hb * HB + r, col, mm, rs, out);
+          continue;
+        }
+        const long long row = (2ll * blk0 + (begins ? 1 : 0)) * 16 + r;
+        float4* a = reinterpret_cast<float4*>(p.part_acc + row * D + col);
+        a[0] = make_float4(out[0], out[1], out[2], out[3]);
+        a[1] = make_float4(out[4], out[5], out[6], out[7]);
+        if (col == 0) {
+          p.part_stat[row] = make_float2(mm, rs);
+        }
+      }
+      if constexpr (CL) {
+        cluster_sync();
+        const uint32_t cs = p.cluster, rank = blockIdx.x % cs;
+        for (uint32_t x = rank * kThreads + threadIdx.x; x < hn * (D / 8); x += cs * kThreads) {
+          const int r = x / (D / 8), col = 8 * (x % (D / 8));
+          if (col >= p.c.d) continue;
+          float2 st[8];
+          float mm = -INFINITY, rs = 0.f, out[8];
+#pragma unroll
+          for (uint32_t c = 0; c < 8; ++c) {
+            st[c] = c < cs ? cluster_load2(stat2 + r, c) : make_float2(-INFINITY, 0.f);
+            mm = fmaxf(mm, st[c].x);
+          }
+          const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out[e] = 0.f;
+#pragma unroll
+          for (uint32_t c = 0; c < 8; ++c) {
+            if (c >= cs) break;
+            const float f = fast_exp2(st[c].x - ref);
+            rs += f * st[c].y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = cluster_load2(acc2 + r * D + col + 2 * e, c);
+              out[2 * e] = fmaf(f, v.x, out[2 * e]);
+              out[2 * e + 1] = fmaf(f, v.y, out[2 * e + 1]);
+            }
+          }
+          write_row(p, b0, hk * p.group + hb * HB + r, col, mm, rs, out);
+        }
+        cluster_sync();  // nobody leaves while the others still read
+      }
+      if (p.batch > kThreads) {
+        __syncthreads();
+        if (p.c.d < D)  // the ring held fp32 sums
+          for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
+    }
+  };
+
+  if constexpr (CL) {
+    const int cs = p.cluster, rank = blockIdx.x % cs, row = blockIdx.x / cs;
+    const int b = row / rows_per_seq, rs = row - b * rows_per_seq;
+    int slot, len;
+    const int tiles = tiles_of<KT>(p, b, &slot, &len);
+    if (threadIdx.x == 0) {
+      sq.len[0] = len;
+      sq.slot[0] = slot;
+      sq.tiles[0] = tiles;
+    }
+    __syncthreads();
+    const uint32_t n = tiles;
+    walk(b, Cursor{rank * kWarps + warp, 0, n, 0, rs, rs / p.head_blocks}, n, cs * kWarps, true);
+    return;
+  }
+
   uint32_t sum = 0, part = 0;  // spans of one row per sequence
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     part = scan(load_seq(b0 + threadIdx.x));
@@ -260,19 +740,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   const Shares sh(W, min(max(W, 1u), static_cast<uint32_t>(p.shares)));
   // few shares: one or two warps of a block, so that they spread over the SMs
   const uint32_t active = sh.n <= grid ? 1 : sh.n <= 2 * grid ? 2 : kWarps;
-  const uint32_t blk0 = blockIdx.x * active;
-  const uint32_t share = warp < active ? blk0 + warp : sh.n;
-  const uint32_t lo = share < sh.n ? sh.begin(share) : W, hi = share < sh.n ? sh.begin(share + 1) : W;
+  blk0 = blockIdx.x * active;
+  share = warp < active ? blk0 + warp : sh.n;
+  lo = share < sh.n ? sh.begin(share) : W;
+  const uint32_t hi = share < sh.n ? sh.begin(share + 1) : W;
   // the block's own range, where all its warps have a share
   const bool full = active == kWarps && blk0 + kWarps <= sh.n;
-  const uint32_t blk_lo = full ? sh.begin(blk0) : 0, blk_hi = full ? sh.begin(blk0 + kWarps) : 0;
-
-  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
-  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::OFF_VALID) + warp * STAGES;
-
-  if (p.c.d < D)
-    for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
-  __syncwarp();
+  blk_lo = full ? sh.begin(blk0) : 0;
+  blk_hi = full ? sh.begin(blk0 + kWarps) : 0;
 
   uint32_t chunk_lo = 0;  // tile at which this chunk of sequences begins
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
@@ -321,382 +796,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
         end = blk_hi;
         step = kWarps;
       }
-      auto advance = [&](Cursor& c) {  // a tile on; c.f < end afterwards or the cursor is not used
-        c.f += step;
-        if (c.f < c.hi || c.f >= end) return;
-        c.lo = c.f = c.hi + kRowCost;
-        if (c.f >= end) return;
-        if (++c.rs == rows_per_seq) {
-          c.rs = 0;
-          do ++c.j;
-          while (sq.tiles[c.j] == 0);
-        }
-        c.hk = p.head_blocks == 1 ? c.rs : c.rs / p.head_blocks;
-        c.hi = c.lo + sq.tiles[c.j];
-      };
-      if (at.f >= at.hi) {  // the share begins behind a row's last tile
-        at.f = at.hi - 1;
-        advance(at);
-      }
-
-      // Page and row of this lane's key (lane & (KT - 1)) of the cursor's tile,
-      // and the tile's K / V head.  The table cell is asked for a round before
-      // copies need it, and nothing is computed from it until then.
-      struct Key {
-        int page, row, hk;
-      };
-      auto locate = [&](const Cursor& c) -> Key {
-        Key r{-1, 0, c.hk};
-        if (c.f >= end) return r;
-        if (c.f == c.lo || c.f == at.f) {
-          // a row begins: its Q into L2, a 128-byte line a lane
-          const int hb = c.rs - c.hk * p.head_blocks, lines = (2 * p.c.d + 127) / 128;
-          const int h = lane / lines;
-          if (h < min(HB, p.group - hb * HB))
-            prefetch_l2(p.q + (b0 + c.j) * p.q_batch + (c.hk * p.group + hb * HB + h) * p.q_head +
-                        (lane - h * lines) * 64);
-        }
-        const Visible vis = visible_of(sq.len[c.j], p.window, p.sinks);
-        const int u = static_cast<int>(c.f - c.lo) * KT + (lane & (KT - 1));
-        if (u < vis.count) {
-          const int j = vis.key(u);
-          const int cell = j / p.c.page_size;
-          r.row = j - cell * p.c.page_size;
-          r.page = p.c.table[static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell];
-        }
-        return r;
-      };
-      // copies of one tile into a stage: whole rows, 16 bytes a lane
-      auto load = [&](int stage, const Key& r) {
-        constexpr int CH = D / 8, RPI = 32 / CH;  // pieces of a row, rows per step
-        const int c = lane % CH;
-        const uint32_t kdst = ring + stage * C::STAGE, vdst = kdst + KT * C::ROW;
-        const uint32_t live = __ballot_sync(0xffffffffu, r.page >= 0 && r.page < p.c.pages);
-        if (lane == 0) valid[stage] = live;
-        const bool col_ok = 8 * c < p.c.d;  // past d the ring holds zeros
-        const __nv_bfloat16* kh = p.k + r.hk * p.c.k_head + 8 * c;
-        const __nv_bfloat16* vh = p.v + r.hk * p.c.v_head + 8 * c;
-        // Most tiles are one run of consecutive rows, or two (where the tile crosses
-        // a page, or from the first tokens into the window): one or two places to
-        // start from instead of one per row.  (With two places for every tile, d =
-        // 256 took 119 us where it takes 93.)
-        const int x = lane & (KT - 1);
-        const int page0 = __shfl_sync(0xffffffffu, r.page, 0), row0 = __shfl_sync(0xffffffffu, r.row, 0);
-        const uint32_t other = __ballot_sync(0xffffffffu, r.page != page0 || r.row != row0 + x);
-        const bool all_live = live == 0xffffffffu;
-        const int row_l = lane / CH;
-        const __nv_bfloat16* k0 = kh + page0 * p.c.k_page + (row0 + row_l) * p.c.k_row;
-        const __nv_bfloat16* v0 = vh + page0 * p.c.v_page + (row0 + row_l) * p.c.v_row;
-        if (all_live && other == 0u) {
-#pragma unroll
-          for (int s = 0; s < KT / RPI; ++s) {
-            const int row = s * RPI + row_l;
-            const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
-            if (!col_ok) break;
-            cp_async16(kdst + dst, k0 + s * RPI * p.c.k_row, true);
-            cp_async16(vdst + dst, v0 + s * RPI * p.c.v_row, true);
-          }
-          return;
-        }
-        const int cut = other ? __ffs(other) - 1 : 0;  // first row of the second run
-        const int page1 = __shfl_sync(0xffffffffu, r.page, cut);
-        const int row1 = __shfl_sync(0xffffffffu, r.row, cut) - cut;
-        if (__all_sync(0xffffffffu, all_live && (x < cut || (r.page == page1 && r.row == row1 + x)))) {
-          const __nv_bfloat16* k1 = kh + page1 * p.c.k_page + (row1 + row_l) * p.c.k_row;
-          const __nv_bfloat16* v1 = vh + page1 * p.c.v_page + (row1 + row_l) * p.c.v_row;
-#pragma unroll
-          for (int s = 0; s < KT / RPI; ++s) {
-            const int row = s * RPI + row_l;
-            const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
-            if (!col_ok) break;
-            cp_async16(kdst + dst, (row < cut ? k0 : k1) + s * RPI * p.c.k_row, true);
-            cp_async16(vdst + dst, (row < cut ? v0 : v1) + s * RPI * p.c.v_row, true);
-          }
-        } else {
-#pragma unroll
-          for (int s = 0; s < KT / RPI; ++s) {
-            const int row = s * RPI + lane / CH;
-            const int page = __shfl_sync(0xffffffffu, r.page, row), at_row = __shfl_sync(0xffffffffu, r.row, row);
-            const bool ok = (live >> row) & 1u;
-            const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
-            if (!col_ok) continue;
-            cp_async16(kdst + dst, ok ? kh + page * p.c.k_page + at_row * p.c.k_row : p.k, ok);
-            cp_async16(vdst + dst, ok ? vh + page * p.c.v_page + at_row * p.c.v_row : p.v, ok);
-          }
-        }
-      };
-
-      Cursor fill = at;
-      {
-        Key ahead[STAGES - 1];
-        bool ahead_live[STAGES - 1];
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) {
-          ahead_live[s] = fill.f < end;
-          ahead[s] = locate(fill);
-          advance(fill);
-        }
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) {
-          if (ahead_live[s]) load(s, ahead[s]);
-          cp_async_commit();
-        }
-      }
-      Key next = locate(fill);
-
-      uint32_t qb[NB][D / 16][2];  // Q as the B operand: column g is a head
-      float o[NB][D / 16][4];      // O^T: rows g, g + 8 of 16 columns of V; heads 2 q4, 2 q4 + 1
-      float m[NB][2], l[NB][2];    // of those heads; l: this lane's keys alone
-      bool begin = true;
-      int stage = 0;
-      while (at.f < end) {
-        // the next free stage was read in the previous round
-        __syncwarp();
-        if (fill.f < end) load(stage == 0 ? STAGES - 1 : stage - 1, next);
-        cp_async_commit();
-        advance(fill);
-        next = locate(fill);
-        const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
-        const int h0 = hk * p.group + hb * HB;      // first query head of the row
-        const int hn = min(HB, p.group - hb * HB);  // its query heads
-        const int b = b0 + at.j;
-        if (begin) {
-          // Q: zero past the row's heads and past d
-          const __nv_bfloat16* q0 = p.q + b * p.q_batch + h0 * p.q_head;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const int h = 8 * nb + g;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int col = 16 * kk + 8 * u + 2 * q4;
-                qb[nb][kk][u] = h < hn && col < p.c.d
-                                    ? *reinterpret_cast<const uint32_t*>(q0 + h * p.q_head + col)
-                                    : 0u;
-              }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) o[nb][i][u] = 0.f;
-            m[nb][0] = m[nb][1] = -INFINITY;
-            l[nb][0] = l[nb][1] = 0.f;
-          }
-          begin = false;
-        }
-        cp_async_wait<STAGES - 1>();
-        __syncwarp();
-        const uint32_t kbase = ring + stage * C::STAGE, vbase = kbase + KT * C::ROW;
-        const uint32_t live = valid[stage];
-        constexpr int MT = KT / 16;  // 16-key rows of S^T
-        // two sums per score, over the even and the odd steps: half the chain
-        float s[MT][NB][4], s1[MT][NB][4];
-#pragma unroll
-        for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) s[kt][nb][u] = s1[kt][nb][u] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int kt = 0; kt < MT; ++kt) {
-            uint32_t ka[4];
-            const int row = kt * 16 + (lane & 15), ch = 2 * kk + (lane >> 4);
-            ldsm_x4(kbase + row * C::ROW + ((ch ^ (row & 7)) << 4), ka);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma16816(kk & 1 ? s1[kt][nb] : s[kt][nb], ka, qb[nb][kk][0], qb[nb][kk][1]);
-          }
-#pragma unroll
-        for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) s[kt][nb][u] += s1[kt][nb][u];
-        constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
-        if ((live & kAll) != kAll) {
-#pragma unroll
-          for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                s[kt][nb][u] = (live >> (16 * kt + g + 8 * (u >> 1))) & 1u ? s[kt][nb][u] : -INFINITY;
-        }
-        // Online softmax over the tile's keys, per head of this lane's pair; P is
-        // rounded to bf16 for the second product, as in the other attention
-        // kernels, and turned from rows of keys to columns (the B operand); the
-        // row sum keeps the unrounded values
-        uint32_t pb[NB][MT][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float alpha[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int kt = 0; kt < MT; ++kt) mx = fmax3(mx, s[kt][nb][u], s[kt][nb][u + 2]);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float m_new = fmaxf(m[nb][u], mx * p.scale_log2);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            alpha[u] = fast_exp2(m[nb][u] - ref);
-            m[nb][u] = m_new;
-            float sum = 0.f;
-#pragma unroll
-            for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float e = fast_exp2(fmaf(s[kt][nb][u + 2 * r], p.scale_log2, -ref));
-                s[kt][nb][u + 2 * r] = e;
-                sum += e;
-              }
-            l[nb][u] = l[nb][u] * alpha[u] + sum;
-          }
-          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) o[nb][i][u] *= alpha[u & 1];
-          }
-#pragma unroll
-          for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              pb[nb][kt][r] = transpose8x8(pack_bf16(s[kt][nb][2 * r], s[kt][nb][2 * r + 1]));
-        }
-#pragma unroll
-        for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-          for (int dd = 0; dd < D / 16; ++dd) {
-            uint32_t va[4];
-            const int row = kt * 16 + (lane & 7) + (lane >> 4) * 8, ch = 2 * dd + ((lane >> 3) & 1);
-            ldsm_x4_trans(vbase + row * C::ROW + ((ch ^ (row & 7)) << 4), va);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][dd], va, pb[nb][kt][0], pb[nb][kt][1]);
-          }
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-
-        const uint32_t f1 = at.f + 1;
-        if (block_row) {
-          if (at.f + step < end) {
-            advance(at);
-            continue;
-          }
-          break;  // the warps' parts of this row meet below
-        } else if (f1 == at.hi || f1 == end) {
-          // the row ends, or the share: the whole row goes to O and LSE, a part of
-          // it to the share's partial results, index 1 where the row begins in
-          // this share, 0 where it goes on
-          const bool begins = at.lo >= lo, whole = begins && f1 == at.hi;
-          const long long pr = (2ll * share + (begins ? 1 : 0)) * 16;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float inv[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              l[nb][u] = sum_rows(l[nb][u]);
-              inv[u] = l[nb][u] > 0.f ? 1.f / l[nb][u] : 0.f;
-              const int h = 8 * nb + 2 * q4 + u;
-              if (g == 0 && h < hn) {
-                if (whole)
-                  p.lse[static_cast<long long>(b) * p.heads + h0 + h] =
-                      l[nb][u] > 0.f ? (m[nb][u] + log2f(l[nb][u])) * kLn2 : -INFINITY;
-                else
-                  p.part_stat[pr + h] = make_float2(m[nb][u], l[nb][u]);
-              }
-            }
-            if (whole) {
-              // pairs of columns of V for head g, out of pairs of heads
-              __nv_bfloat16* dst = p.o + b * p.o_batch + (h0 + 8 * nb + g) * p.o_head + 2 * q4;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const uint32_t x =
-                      transpose8x8(pack_bf16(o[nb][i][2 * r] * inv[0], o[nb][i][2 * r + 1] * inv[1]));
-                  const int col = 16 * i + 8 * r;
-                  if (8 * nb + g < hn && col < p.c.d) *reinterpret_cast<uint32_t*>(dst + col) = x;
-                }
-            } else {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int h = 8 * nb + 2 * q4 + u;
-                float* dst = p.part_acc + (pr + h) * D + g;
-                if (h < hn)
-#pragma unroll
-                  for (int i = 0; i < D / 16; ++i) {
-                    dst[16 * i] = o[nb][i][u];
-                    dst[16 * i + 8] = o[nb][i][2 + u];
-                  }
-              }
-            }
-          }
-          begin = true;
-        }
-        advance(at);
-      }
-      cp_async_wait<0>();
-      if (block_row) {
-        // one partial result for the block, in its first share's place: a quarter
-        // of what the joining kernel would read
-        const int hk = at.hk, hb = at.rs - hk * p.head_blocks;
-        const int hn = min(HB, p.group - hb * HB);
-        constexpr int LD = D + 4;  // (a warp's eight heads in different banks)
-        __syncthreads();
-        float2* stat = reinterpret_cast<float2*>(smem);  // [warp][HB], then [warp][HB][LD] sums
-        float* acc = reinterpret_cast<float*>(smem + kWarps * HB * sizeof(float2));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int h = warp * HB + 8 * nb + 2 * q4 + u;
-            const float sum = sum_rows(l[nb][u]);
-            if (g == 0) stat[h] = make_float2(m[nb][u], sum);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              acc[h * LD + 16 * i + g] = o[nb][i][u];
-              acc[h * LD + 16 * i + 8 + g] = o[nb][i][2 + u];
-            }
-          }
-        __syncthreads();
-        const bool begins = at.lo >= blk_lo, whole = begins && at.hi == blk_hi;
-        for (int x = threadIdx.x; x < hn * (D / 8); x += kThreads) {
-          const int r = x / (D / 8), col = 8 * (x % (D / 8));
-          float mm = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * HB + r].x);
-          const float ref = mm == -INFINITY ? 0.f : mm;
-          float rs = 0.f, out[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) out[e] = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 st = stat[w * HB + r];
-            const float f = fast_exp2(st.x - ref);
-            rs += f * st.y;
-            add_row8(out, f, acc + (w * HB + r) * LD + col);
-          }
-          if (whole) {
-            if (col < p.c.d) write_row(p, b0 + at.j, hk * p.group + hb * HB + r, col, mm, rs, out);
-            continue;
-          }
-          const long long row = (2ll * blk0 + (begins ? 1 : 0)) * 16 + r;
-          float4* a = reinterpret_cast<float4*>(p.part_acc + row * D + col);
-          a[0] = make_float4(out[0], out[1], out[2], out[3]);
-          a[1] = make_float4(out[4], out[5], out[6], out[7]);
-          if (col == 0) {
-            p.part_stat[row] = make_float2(mm, rs);
-          }
-        }
-        if (p.batch > kThreads) {
-          __syncthreads();
-          if (p.c.d < D)  // the ring held fp32 sums
-            for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
-          __syncwarp();
-        }
-      }
+      walk(b0, at, end, step, block_row);
     }
     chunk_lo = chunk_hi;
     if (p.batch > kThreads) __syncthreads();  // the next chunk overwrites the sequences
@@ -830,6 +930,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
 // joined, where none can have more than one tile.
 struct Plan {
   long long tiles;  // at most, of the whole batch
+  int cluster;      // > 0: a cluster of that many blocks per row
   long long grid;
   bool cut;
   size_t off_acc, bytes;
@@ -858,8 +959,19 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const long long rows = static_cast<long long>(batch) * c.heads_kv * ((G + HB - 1) / HB);
   Plan p;
   p.tiles = rows * (tiles + kRowCost);
-  p.grid = p.tiles < 148ll * per_sm ? p.tiles : 148ll * per_sm;
-  p.cut = tiles > 1;
+  // A cluster per row where all rows' clusters are resident at once (not every
+  // slot of the GPU can be in a cluster of 8) and a warp's tiles then are at most
+  // four more than in equal shares: the time that joining and working out the
+  // shares take.
+  int cs = 8;
+  while (cs > 1 && rows * cs > 128ll * per_sm) cs /= 2;
+  while (cs > 1 && tiles <= cs / 2 * kWarps) cs /= 2;  // no warps without tiles
+  const long long equal = (p.tiles + 148ll * per_sm * kWarps - 1) / (148ll * per_sm * kWarps);
+  p.cluster = rows * cs <= 128ll * per_sm && (tiles + cs * kWarps - 1) / (cs * kWarps) <= equal + 4 ? cs : 0;
+  p.grid = p.cluster > 0                  ? rows * p.cluster
+           : p.tiles < 148ll * per_sm ? p.tiles
+                                      : 148ll * per_sm;
+  p.cut = p.cluster == 0 && tiles > 1;
   const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
   p.off_acc = parts * sizeof(float2);
   p.bytes = p.cut ? p.off_acc + parts * D * sizeof(float) : 0;
@@ -870,10 +982,16 @@ template <int D, int NB>
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t stream) {
   using C = DecodeCfg<D, NB>;
   static_assert(kWarps * 8 * NB * (8 + (D + 4) * 4) <= C::OFF_VALID, "a block's parts fit the ring");
-  auto kern = attend_kernel<D, NB>;
+  auto kern = attend_kernel<D, NB, false>;
+  auto kern_cl = attend_kernel<D, NB, true>;
+  static_assert(kWarps * 8 * NB * (8 + (D + 4) * 4) + 8 * NB * (8 + D * 4) <= C::OFF_VALID,
+                "and the cluster's");
   static OncePerContext prepared;
   const cudaError_t e = prepared.run([&]() -> cudaError_t {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t first = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(C::SMEM));
+    if (first != cudaSuccess) return first;
+    return cudaFuncSetAttribute(kern_cl, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(C::SMEM));
   });
   if (e != cudaSuccess) return e;
@@ -881,6 +999,22 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
   AttendParams a = p;
   a.grid = static_cast<uint32_t>(plan.grid);
   a.shares = static_cast<int>(plan.grid) * kWarps;
+  a.cluster = plan.cluster;
+  if (plan.cluster > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(plan.cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern_cl, a);
+  }
   if (plan.cut) {
     char* ws = static_cast<char*>(workspace);
     a.part_stat = reinterpret_cast<float2*>(ws);

@@ -487,3 +487,48 @@ def test_attend_leads_to_the_next_call_in_order(lib):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         cache.k.copy_(keep[0])
         cache.v.copy_(keep[1])
+
+
+def widened(lib, cache, columns=40000):
+    """The same cache with room for very long sequences: the work is then cut into
+    equal shares, where short tables get a cluster of blocks per row."""
+    table = torch.full((cache.slots, columns), -1, dtype=torch.int32, device="cuda")
+    table[:, :cache.max_pages] = cache.table
+    return lib.PagedCache(cache.k, cache.v, table, cache.lengths, cache.refs)
+
+
+@pytest.mark.parametrize("lens,P,H,Hkv,d,window,sinks,order", DECODE)
+def test_attend_in_equal_shares(lib, lens, P, H, Hkv, d, window, sinks, order):
+    small = filled(lib, lens, P, Hkv, d, seed=len(lens) + d + 1, order=order)
+    cache = widened(lib, small, 40000 if P <= 256 else 4000)
+    q = randn((len(lens), H, d), 51)
+    o, lse = cache.attend(0, q, window=window, sinks=sinks)
+    check_attend(cache, 0, q, None, o, lse, d ** -0.5, window, sinks)
+    o2, lse2 = cache.attend(0, q, window=window, sinks=sinks)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_equal_shares_with_holes_and_bad_lengths(lib):
+    cache = widened(lib, filled(lib, [100, 90, 64, 64, 40], 16, 2, 64, seed=4))
+    cache.table[0, 2] = -1
+    cache.table[0, 6] = cache.pages
+    cache.table[1, :] = -1
+    cache.lengths[2] = -1
+    cache.lengths[3] = -5
+    cache.table[4, 0] = -7
+    q = randn((5, 4, 64), 61)
+    o, lse = cache.attend(0, q)
+    check_attend(cache, 0, q[[0, 4]], [0, 4], o[[0, 4]], lse[[0, 4]], 0.125)
+    for i in (1, 2, 3):
+        assert (o[i] == 0).all() and (lse[i] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("B,Hkv,longest", [(1, 1, 700), (3, 8, 100), (30, 4, 60), (64, 4, 200), (40, 1, 2000)])
+def test_attend_cluster_sizes(lib, B, Hkv, longest):
+    """Rows in clusters of 8 down to 1 block, some with fewer tiles than warps."""
+    r = random.Random(B)
+    lens = [r.randint(0, longest) for _ in range(B - 1)] + [longest]
+    cache = filled(lib, lens, 16, Hkv, 128, seed=B + 1)
+    q = randn((B, 5 * Hkv, 128), 66)
+    o, lse = cache.attend(0, q)
+    check_attend(cache, 0, q, None, o, lse, 128 ** -0.5)
