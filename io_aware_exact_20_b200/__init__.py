@@ -361,18 +361,15 @@ def wait_timeout_probe(device=None):
 # ---------------------------------------------------------------------------
 
 def _strides(t, layout):
-    if t is None:
-        return Strides(0, 0, 0)
+    """Element strides (batch, head, row) of a tensor in the layout."""
     s = t.stride()
     if s[-1] != 1:
         raise ValueError("the head dimension must be contiguous")
     if layout == "bhsd":
-        return Strides(s[0], s[1], s[2])
+        return s[:3]
     if layout == "bshd":
-        return Strides(s[0], s[2], s[1])
-    if layout == "thd":
-        return Strides(0, s[1], s[0])
-    raise ValueError(f"unknown layout {layout!r}")
+        return s[0], s[2], s[1]
+    return 0, s[1], s[0]
 
 
 def _dims(t, layout):
@@ -386,6 +383,7 @@ def _dims(t, layout):
 
 # the tensors of a call that have Q's shape; the others (k, v, dk, dv) have K's
 _Q_SIDE = ("q", "o", "dout", "dq")
+_UNUSED = (0, 0, 0)
 
 
 def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
@@ -395,53 +393,44 @@ def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, 
     if layout not in ("bhsd", "bshd", "thd"):
         raise ValueError(f"unknown layout {layout!r}")
     want_dim = 3 if layout == "thd" else 4
-    device, shape_q, shape_k = q.device, q.shape, k.shape
+    device, index, bf16, shape_q, shape_k = q.device, q.get_device(), torch.bfloat16, q.shape, k.shape
     for name, t in tensors.items():
-        if t.dim() != want_dim:
+        shape, ref = t.shape, shape_q if name in _Q_SIDE else shape_k
+        if len(shape) != want_dim:
             raise ValueError(f"{name}: a {want_dim}-D tensor is expected for layout {layout!r}")
-        if not t.is_cuda or t.dtype is not torch.bfloat16 or t.device != device:
+        if index < 0 or t.get_device() != index or t.dtype is not bf16:
             raise ValueError(f"{name}: bfloat16 on the device of q is expected")
-        ref = q if name in _Q_SIDE else k
-        if t.shape != (shape_q if name in _Q_SIDE else shape_k):
-            raise ValueError(f"{name}: shape {tuple(t.shape)} differs from "
-                             f"{'q' if name in _Q_SIDE else 'k'} {tuple(ref.shape)}")
+        if shape != ref:
+            raise ValueError(f"{name}: shape {tuple(shape)} differs from "
+                             f"{'q' if name in _Q_SIDE else 'k'} {tuple(ref)}")
     Bq, Nq, H, d = _dims(q, layout)
     Bk, Nk, Hk, dk = _dims(k, layout)
     if d != dk or Hk < 1 or H % Hk:
         raise ValueError("q and k must have the same head dim, and q's heads must be a multiple "
                          "of k's (grouped-query attention)")
-    keep = []
-    a = AttentionDesc()
-    a.heads, a.head_dim, a.heads_kv = H, d, Hk
+    cq = ck = None
     if layout == "thd":
         if cu_seqlens_q is None or cu_seqlens_k is None:
             raise ValueError("the packed layout needs cu_seqlens_q and cu_seqlens_k")
-        cq = _array(cu_seqlens_q, torch.int32, device)
-        ck = _array(cu_seqlens_k, torch.int32, device)
-        keep += [cq, ck]
-        a.batch = cq.numel() - 1
-        a.cu_seqlens_q, a.cu_seqlens_k = cq.data_ptr(), ck.data_ptr()
-        a.total_q, a.total_k = Nq, Nk
         if max_seqlen_q is None or max_seqlen_k is None:
             raise ValueError("the packed layout needs max_seqlen_q and max_seqlen_k")
-        a.seqlen_q, a.seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
+        cq = _array(cu_seqlens_q, torch.int32, device)
+        ck = cq if cu_seqlens_k is cu_seqlens_q else _array(cu_seqlens_k, torch.int32, device)
+        sizes = (cq.numel() - 1, H, d, int(max_seqlen_q), int(max_seqlen_k), cq.data_ptr(),
+                 ck.data_ptr(), Nq, Nk)
     else:
         if Bq != Bk:
             raise ValueError("q and k must have the same batch size")
-        a.batch, a.seqlen_q, a.seqlen_k = Bq, Nq, Nk
-    sl, bm = _masks(seqlens_k, block_mask, q.device)
-    keep += [sl, bm]
-    a.seqlens_k = _ptr(sl)
-    a.block_mask = _ptr(bm)
-    a.softmax_scale = float(d ** -0.5 if scale is None else scale)
-    a.causal = int(bool(causal))
-    a.dropout_p = float(dropout_p)
-    a.seed = int(seed) & 0xFFFFFFFFFFFFFFFF
-    a.dropout_row0, a.dropout_key0 = (int(x) for x in dropout_pos)
-    a.window, a.sinks = _window(window, sinks)
-    for name, t in tensors.items():
-        setattr(a, name, _strides(t, layout))
-    return a, keep
+        sizes = (Bq, H, d, Nq, Nk, None, None, 0, 0)
+    sl, bm = _masks(seqlens_k, block_mask, device)
+    strides = {name: _strides(t, layout) for name, t in tensors.items()}
+    # the fields in their order: one call instead of a Python step for each
+    a = AttentionDesc(*sizes, _ptr(sl), float(d ** -0.5 if scale is None else scale),
+                      int(bool(causal)), float(dropout_p), int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(bm),
+                      *[strides.get(name, _UNUSED)
+                        for name in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")],
+                      int(dropout_pos[0]), int(dropout_pos[1]), Hk, *_window(window, sinks))
+    return a, (cq, ck, sl, bm)
 
 
 def _window(window, sinks):
@@ -480,10 +469,11 @@ def forward_general(q, k, v, *, layout="bhsd", cu_seqlens_q=None, cu_seqlens_k=N
                     causal, seqlens_k, dropout_p, seed, block_mask,
                     dict(q=q, k=k, v=v, o=out), (dropout_row0, dropout_key0), window, sinks)
     if lse is None:
-        lse = torch.empty(_lse_shape(q, layout), dtype=torch.float32, device=q.device)
-    _check_lse(lse, q, layout)
-    code = library().fa_fwd_ex(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                               _stream_ptr(q.device))
+        lse = q.new_empty(_lse_shape(q, layout), dtype=torch.float32)
+    else:
+        _check_lse(lse, q, layout)
+    code = library().fa_fwd_ex(ctypes.byref(a), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               out.data_ptr(), lse.data_ptr(), _stream_ptr(q.device))
     _check(code, "fa_fwd_ex")
     del keep
     return out, lse
@@ -535,12 +525,15 @@ def backward_general(q, k, v, o, lse, dout, *, layout="bhsd", cu_seqlens_q=None,
     lib = library()
     need = int(lib.fa_bwd_ex_workspace_size(ctypes.byref(a)))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        nbytes = max((need + 3) // 4, 1) * 4
+        workspace = lse.new_empty(nbytes // 4)
     elif not workspace.is_cuda or workspace.device != q.device:
         raise ValueError("workspace: a tensor on the device of q is expected")
-    code = lib.fa_bwd_ex(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
-                         _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                         workspace.numel() * workspace.element_size(), _stream_ptr(q.device))
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    code = lib.fa_bwd_ex(ctypes.byref(a), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                         lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                         dv.data_ptr(), workspace.data_ptr(), nbytes, _stream_ptr(q.device))
     _check(code, "fa_bwd_ex")
     del keep
     return dq, dk, dv
