@@ -250,7 +250,7 @@ fa_status_t fa_fwd_ex(const fa_attention_desc_t* desc, const void* q, const void
  * (few units for the SM count), two fp32 dK / dV areas of
  * S * tb * heads_kv * key rows * D elements more (tb = B padded, 1 packed; key
  * rows = seqlen_k padded, total_k packed); with a window and first tokens, two
- * fp32 areas of the first tokens' partial dK / dV more, at most 1184 * 128 * D
+ * fp32 areas of the first tokens' partial dK / dV more, at most 1776 * 128 * D
  * elements each.  0 if the description is invalid. */
 size_t fa_bwd_ex_workspace_size(const fa_attention_desc_t* desc);
 

@@ -532,3 +532,28 @@ def test_attend_cluster_sizes(lib, B, Hkv, longest):
     q = randn((B, 5 * Hkv, 128), 66)
     o, lse = cache.attend(0, q)
     check_attend(cache, 0, q, None, o, lse, 128 ** -0.5)
+
+
+def test_extend_by_far_too_much(lib):
+    """Token counts up to the largest int are refused entry by entry."""
+    cache = make(lib, pages=20, P=4, slots=5, max_pages=8)
+    model = CacheModel(cache)
+    slots, tokens = [0, 1, 2, 3], [2 ** 31 - 1, 33, 32, -2 ** 31]
+    assert cache.extend(ints(slots), ints(tokens)).tolist() == model.extend(slots, tokens) == [-1, -1, 0, -1]
+    model.check(cache)
+    # a slot at its end stays there, and a row of its pages cannot grow
+    assert cache.extend(ints([2]), ints([1])).tolist() == [-1]
+    assert cache.extend(ints([2]), ints([0])).tolist() == [32]
+    model.check(cache)
+
+
+def test_attend_into_its_own_queries(lib):
+    """O may be Q's memory: every query is read before its row is written."""
+    for lens, columns in (([300, 40, 7], None), ([300, 40, 7, 20000], 40000)):
+        cache = filled(lib, lens, 16, 2, 128, seed=31)
+        if columns:
+            cache = widened(lib, cache, columns)
+        q = randn((len(lens), 8, 128), 67)
+        want = cache.attend(0, q)
+        cache.attend(0, q, out=q)
+        assert torch.equal(q, want[0])

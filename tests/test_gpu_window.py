@@ -231,3 +231,21 @@ def test_own_key_alone_has_no_score_gradient(lib, d, Hkv, p):
     assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
     if not p:
         assert torch.equal(got["o"], v.repeat_interleave(H // Hkv, 1))
+
+
+@pytest.mark.parametrize("d,H,Hkv", [(64, 2, 1), (128, 2, 2)])
+def test_window_with_dropout_positions(lib, d, H, Hkv):
+    """The keep bits are keyed by the block's place in a longer sequence; the
+    window counts the call's own rows."""
+    import numpy as np
+    import oracle
+    N, p, seed, row0, key0, window, sinks = 300, 0.3, 5, 77, 128, 60, 3
+    q, do = randn((1, H, N, d), 94), randn((1, H, N, d), 95)
+    k, v = randn((1, Hkv, N, d), 96), randn((1, Hkv, N, d), 97)
+    keep = np.stack([oracle.dropout_keep(seed, p, 0, h, np.arange(row0, row0 + N), N, key0=key0) for h in range(H)])
+    keep = torch.from_numpy(keep)[None].cuda()
+    ref = plain64.padded(q, k, v, d ** -0.5, lambda b: plain64.visible(
+        N, N, q.device, window=window, sinks=sinks), do, keep, oracle.dropout_scale(p))
+    got = run(lib, q, k, v, do, causal=True, window=window, sinks=sinks, dropout_p=p, seed=seed,
+              dropout_row0=row0, dropout_key0=key0)
+    compare(got, ref)
