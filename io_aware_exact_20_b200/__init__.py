@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 from .build import LIB_PATH
 
@@ -113,6 +114,9 @@ class CacheDesc(ctypes.Structure):
         ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("refs", ctypes.c_void_p),
     ]
 
+
+# AttentionDesc's fields in order, with native alignment
+_DESC = struct.Struct("@iiiiiPPiiPfifQP24qqqiii0q")
 
 _DP = ctypes.POINTER(AttentionDesc)
 _CP = ctypes.POINTER(CacheDesc)
@@ -421,15 +425,16 @@ def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, 
     else:
         if Bq != Bk:
             raise ValueError("q and k must have the same batch size")
-        sizes = (Bq, H, d, Nq, Nk, None, None, 0, 0)
+        sizes = (Bq, H, d, Nq, Nk, 0, 0, 0, 0)
     sl, bm = _masks(seqlens_k, block_mask, device)
-    strides = {name: _strides(t, layout) for name, t in tensors.items()}
-    # the fields in their order: one call instead of a Python step for each
-    a = AttentionDesc(*sizes, _ptr(sl), float(d ** -0.5 if scale is None else scale),
-                      int(bool(causal)), float(dropout_p), int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(bm),
-                      *[strides.get(name, _UNUSED)
-                        for name in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")],
-                      int(dropout_pos[0]), int(dropout_pos[1]), Hk, *_window(window, sinks))
+    get = {name: _strides(t, layout) for name, t in tensors.items()}.get
+    # all fields at once (4 us less than one by one)
+    a = AttentionDesc.from_buffer_copy(_DESC.pack(
+        *sizes, _ptr(sl) or 0, d ** -0.5 if scale is None else scale, bool(causal), dropout_p,
+        int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(bm) or 0, *get("q", _UNUSED), *get("k", _UNUSED),
+        *get("v", _UNUSED), *get("o", _UNUSED), *get("dout", _UNUSED), *get("dq", _UNUSED),
+        *get("dk", _UNUSED), *get("dv", _UNUSED), int(dropout_pos[0]), int(dropout_pos[1]), Hk,
+        *_window(window, sinks)))
     return a, (cq, ck, sl, bm)
 
 

@@ -525,10 +525,9 @@ fa_status_t run_bwd(const Problem& pr, const void* q, const void* k, const void*
   if (fa::launch_bwd_main(pr.D, p.drop_threshold != 0, m.q, m.k, m.v, m.dout, m.dq, p, s) !=
       cudaSuccess)
     return FA_ERR_CUDA;
-  if (fa::launch_bwd_post(pr.D, p, s) != cudaSuccess) return FA_ERR_CUDA;
-  if (p.split > 1 && fa::launch_bwd_kv_post(pr.D, p, s) != cudaSuccess) return FA_ERR_CUDA;
-  if (p.sink_tiles > 0 && fa::launch_bwd_sink_post(pr.D, p, s) != cudaSuccess) return FA_ERR_CUDA;
-  return FA_OK;
+  const cudaError_t e = p.split > 1 || p.sink_tiles > 0 ? fa::launch_bwd_post_all(pr.D, p, s)
+                                                       : fa::launch_bwd_post(pr.D, p, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

@@ -284,15 +284,13 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
   }
 }
 
+// dQ = bf16(scale * accumulator) of row block bx of (b, h) = bh.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_post_kernel(const BwdParams p) {
+__device__ __forceinline__ void post_dq(const BwdParams& p, int bx, int bh) {
   constexpr int G = D / 8;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int bh = blockIdx.y;
   const int b = bh / p.H, h = bh % p.H;
   const Seq sq = seq_of(p.rows, b);
-  const int i = blockIdx.x * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
+  const int i = bx * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
   const int part = static_cast<int>(threadIdx.x) % G;
   if (i >= sq.lq || part * 8 >= p.d_real) return;
   const long long acc_off = (ws_row0(p, b, h, sq.q0) + i) * D + part * 8;
@@ -312,19 +310,23 @@ __global__ void __launch_bounds__(256) bwd_post_kernel(const BwdParams p) {
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + dq_off) = out;
 }
 
-// dK, dV = bf16(sum over the parts' fp32 slices) of split units (grouped K / V
-// heads), the parts added in order: grid (blocks of kRowsPerBlock<D> key rows
-// of the longest sequence) x (B * H_kv).  The slices hold scaled gradients.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_kv_post_kernel(const BwdParams p) {
-  constexpr int G = D / 8;
+__global__ void __launch_bounds__(256) bwd_post_kernel(const BwdParams p) {
   griddep_wait();
   griddep_launch_dependents();
+  post_dq<D>(p, blockIdx.x, blockIdx.y);
+}
+
+// dK, dV = bf16(sum over the parts' fp32 slices) of split units (grouped K / V
+// heads), the parts added in order: key row block bx of (b, K / V head) = bh.
+// The slices hold scaled gradients.
+template <int D>
+__device__ __forceinline__ void post_kv(const BwdParams& p, int bx, int bh) {
+  constexpr int G = D / 8;
   const int n_kv = p.H / p.group;
-  const int bh = blockIdx.y;
   const int b = bh / n_kv, hk = bh % n_kv;
   const Seq sq = seq_of(p.rows, b);
-  const int j = blockIdx.x * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
+  const int j = bx * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
   const int part = static_cast<int>(threadIdx.x) % G;
   if (j >= sq.lk || part * 8 >= p.d_real || j < 128 * p.sink_tiles) return;
   const long long rows_k = p.rows.cu_k == nullptr ? p.rows.nk : p.rows.total_k;
@@ -360,18 +362,15 @@ __device__ __forceinline__ int sink_from(int kb, int window, int off, int nqb) {
 }
 
 // dK, dV of the first key tiles = bf16(sum over the slices of their units, the
-// ordinary one first, then the walk's pieces in order): grid (row blocks of
-// those tiles) x (B * H_kv).  The slices hold scaled gradients.
+// ordinary one first, then the walk's pieces in order): row block bx of those
+// tiles of (b, K / V head) = bh.  The slices hold scaled gradients.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_sink_post_kernel(const BwdParams p) {
+__device__ __forceinline__ void post_sink(const BwdParams& p, int bx, int bh) {
   constexpr int G = D / 8;
-  griddep_wait();
-  griddep_launch_dependents();
   const int n_kv = p.H / p.group;
-  const int bh = blockIdx.y;
   const int b = bh / n_kv, hk = bh % n_kv;
   const Seq sq = seq_of(p.rows, b);
-  const int j = blockIdx.x * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
+  const int j = bx * kRowsPerBlock<D> + static_cast<int>(threadIdx.x) / G;
   const int part = static_cast<int>(threadIdx.x) % G;
   if (j >= sq.lk || part * 8 >= p.d_real) return;
   const int nqb = (sq.lq + 127) / 128;
@@ -401,6 +400,28 @@ __global__ void __launch_bounds__(256) bwd_sink_post_kernel(const BwdParams p) {
   };
   cvt(p.ws_sk + acc, static_cast<__nv_bfloat16*>(p.dk) + dk_off);
   cvt(p.ws_sv + acc, static_cast<__nv_bfloat16*>(p.dv) + dv_off);
+}
+
+// All conversions in one launch: dQ's blocks, then those of the split units'
+// dK / dV, then the first keys' (a launch each cost 3 us of latency and 2.4 us
+// of the host).
+template <int D>
+__global__ void __launch_bounds__(256, 4) bwd_post_all_kernel(const BwdParams p, int dq_x, int kv_x,
+                                                             int sink_x) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long n_dq = static_cast<long long>(dq_x) * p.B * p.H;
+  const int n_bkv = p.B * (p.H / p.group);
+  const long long n_kv = static_cast<long long>(kv_x) * n_bkv;
+  long long u = blockIdx.x;
+  if (u < n_dq) {
+    post_dq<D>(p, static_cast<int>(u % dq_x), static_cast<int>(u / dq_x));
+  } else if ((u -= n_dq) < n_kv) {
+    post_kv<D>(p, static_cast<int>(u % kv_x), static_cast<int>(u / kv_x));
+  } else {
+    u -= n_kv;
+    post_sink<D>(p, static_cast<int>(u % sink_x), static_cast<int>(u / sink_x));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1408,6 +1429,19 @@ cudaError_t launch_main_t(const CUtensorMap& tq, const CUtensorMap& tk, const CU
 }
 
 template <int D>
+cudaError_t launch_post_all_t(const BwdParams& p, cudaStream_t stream) {
+  const long long key_rows = (static_cast<long long>(p.rows.nk) + 127) / 128 * 128;
+  const dim3 dq = prepost_grid<D>(p);
+  const int kv_x = p.split > 1 ? static_cast<int>(key_rows / kRowsPerBlock<D>) : 0;
+  const int sink_x = 128 * p.sink_tiles / kRowsPerBlock<D>;
+  const long long blocks = static_cast<long long>(dq.x) * dq.y +
+                           static_cast<long long>(kv_x + sink_x) * p.B * (p.H / p.group);
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  return launch_overlapped(bwd_post_all_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                           stream, p, static_cast<int>(dq.x), kv_x, sink_x);
+}
+
+template <int D>
 cudaError_t launch_post_t(const BwdParams& p, cudaStream_t stream) {
   return launch_overlapped(bwd_post_kernel<D>, prepost_grid<D>(p), dim3(256), 0, stream, p);
 }
@@ -1467,25 +1501,10 @@ cudaError_t launch_bwd_main(int d, bool dropout, const CUtensorMap& tq, const CU
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_bwd_kv_post(int d, const BwdParams& p, cudaStream_t stream) {
-  const long long rows = (static_cast<long long>(p.rows.nk) + 127) / 128 * 128;
-  auto grid = [&](int rpb) {
-    return dim3(static_cast<unsigned>(rows / rpb), static_cast<unsigned>(p.B * (p.H / p.group)), 1);
-  };
-  if (d == 64) return launch_overlapped(bwd_kv_post_kernel<64>, grid(kRowsPerBlock<64>), dim3(256), 0, stream, p);
-  if (d == 128) return launch_overlapped(bwd_kv_post_kernel<128>, grid(kRowsPerBlock<128>), dim3(256), 0, stream, p);
-  if (d == 256) return launch_overlapped(bwd_kv_post_kernel<256>, grid(kRowsPerBlock<256>), dim3(256), 0, stream, p);
-  return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_bwd_sink_post(int d, const BwdParams& p, cudaStream_t stream) {
-  auto grid = [&](int rpb) {
-    return dim3(static_cast<unsigned>(128 * p.sink_tiles / rpb),
-                static_cast<unsigned>(p.B * (p.H / p.group)), 1);
-  };
-  if (d == 64) return launch_overlapped(bwd_sink_post_kernel<64>, grid(kRowsPerBlock<64>), dim3(256), 0, stream, p);
-  if (d == 128) return launch_overlapped(bwd_sink_post_kernel<128>, grid(kRowsPerBlock<128>), dim3(256), 0, stream, p);
-  if (d == 256) return launch_overlapped(bwd_sink_post_kernel<256>, grid(kRowsPerBlock<256>), dim3(256), 0, stream, p);
+cudaError_t launch_bwd_post_all(int d, const BwdParams& p, cudaStream_t stream) {
+  if (d == 64) return launch_post_all_t<64>(p, stream);
+  if (d == 128) return launch_post_all_t<128>(p, stream);
+  if (d == 256) return launch_post_all_t<256>(p, stream);
   return cudaErrorInvalidValue;
 }
 

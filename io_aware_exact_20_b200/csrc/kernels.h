@@ -261,10 +261,9 @@ cudaError_t launch_bwd_main(int d, bool dropout, const CUtensorMap& tq, const CU
                             const CUtensorMap& tv, const CUtensorMap& tdo, const CUtensorMap& tdq,
                             const BwdParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_post(int d, const BwdParams& p, cudaStream_t stream);
-// dK, dV from the fp32 accumulators of split units (BwdParams::split > 1)
-cudaError_t launch_bwd_kv_post(int d, const BwdParams& p, cudaStream_t stream);
-// dK, dV of the first keys from their units' slices (BwdParams::sink_tiles > 0)
-cudaError_t launch_bwd_sink_post(int d, const BwdParams& p, cudaStream_t stream);
+// The dQ conversion with dK, dV from the fp32 slices of split units
+// (BwdParams::split > 1) and of the first keys' units (BwdParams::sink_tiles > 0).
+cudaError_t launch_bwd_post_all(int d, const BwdParams& p, cudaStream_t stream);
 
 // Fused QKV projection (fa_proj.cu): x bf16 [B N, d_model], w bf16
 // [3 H d, d_model], bias bf16 [3 H d] or null -> q, k, v bf16 [B, H, N, d].

@@ -60,3 +60,27 @@ def test_gradients_against_differences():
                 f.append((plain64.head(q, k, v, scale, mask)["o"] * do).sum().item())
                 t.view(-1)[at] -= s
             assert abs((f[0] - f[1]) / (2 * h) - r[name].reshape(-1)[at].item()) < 1e-7
+
+
+def test_packed_description_equals_the_fields(lib):
+    """The binding packs a description's fields in one step: the same bytes as
+    setting them one by one, and the size of the C structure."""
+    assert lib._DESC.size == ctypes.sizeof(lib.AttentionDesc)
+    a = lib.AttentionDesc()
+    values = iter(range(1, 100))
+    flat = []
+    for name, kind in lib.AttentionDesc._fields_:
+        if kind is lib.Strides:
+            s = [next(values) for _ in range(3)]
+            setattr(a, name, lib.Strides(*s))
+            flat += s
+        else:
+            v = next(values)
+            setattr(a, name, v)
+            flat.append(v)
+    b = lib.AttentionDesc.from_buffer_copy(lib._DESC.pack(*flat))
+    for name, kind in lib.AttentionDesc._fields_:
+        x, y = getattr(a, name), getattr(b, name)
+        if kind is lib.Strides:
+            x, y = [(s.batch, s.head, s.row) for s in (x, y)]
+        assert x == y, name
