@@ -40,7 +40,7 @@ class PagedCache:
         self.k, self.v, self.table, self.lengths, self.refs = k, v, table, lengths, refs
         self.layers, self.pages, self.heads_kv, self.page_size, self.head_dim = k.shape
         self.slots, self.max_pages = table.shape
-        self.device, self._row = k.device, (self.heads_kv, self.head_dim)
+        self.device = k.device
         a = _fa.CacheDesc()
         a.layers, a.pages, a.page_size = self.layers, self.pages, self.page_size
         a.heads_kv, a.head_dim = self.heads_kv, self.head_dim
@@ -52,6 +52,7 @@ class PagedCache:
         a.table, a.lengths, a.refs = table.data_ptr(), lengths.data_ptr(), refs.data_ptr()
         self._desc, self._ref = a, ctypes.byref(a)
         self._lib, self._torch, self._index = _fa.library(), torch, k.get_device()
+        self._i32, self._bf16 = torch.int32, torch.bfloat16
         self._sizes = {}
         if self._lib.fa_cache_workspace_size(self._ref, 0) == 0:
             raise ValueError("the cache's sizes, strides or alignment are not supported (fa.h)")
@@ -66,12 +67,20 @@ class PagedCache:
         return cls(*kv, ints(slots, max_pages).fill_(-1), ints(slots), ints(pages))
 
     def _ints(self, name, t, n):
-        if (t.dtype is not self._torch.int32 or t.dim() != 1 or t.get_device() != self._index
+        if (t.dtype is not self._i32 or t.shape != (n,) or t.get_device() != self._index
                 or not t.is_contiguous()):
-            raise ValueError(f"{name}: a contiguous 1-D int32 tensor on the cache's device is expected")
-        if t.shape[0] != n:
-            raise ValueError(f"{name}: {n} entries are expected, got {t.shape[0]}")
+            raise ValueError(f"{name}: a contiguous 1-D int32 tensor of {n} entries on the cache's "
+                             f"device is expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
+
+    def _queries(self, name, t, shape):
+        """The strides of a tensor of the queries' shape."""
+        st = t.stride()
+        if (t.dtype is not self._bf16 or t.get_device() != self._index or t.shape != shape
+                or st[2] != 1):
+            raise ValueError(f"{name}: bfloat16 {tuple(shape)} on the cache's device, d contiguous, "
+                             "is expected")
+        return st
 
     def _workspace(self, n):
         size = self._sizes.get(n)
@@ -94,7 +103,7 @@ class PagedCache:
     def extend(self, slots, tokens):
         """Grows slots[i] by tokens[i]; returns start (int32 [n]), each entry's
         first new position, -1 where it was not granted (fa_cache_extend)."""
-        n = slots.shape[0]
+        n = slots.numel()
         start = self.lengths.new_empty(n)
         ws, size = self._workspace(n)
         self._call(self._lib.fa_cache_extend, self._ints("slots", slots, n),
@@ -106,13 +115,14 @@ class PagedCache:
         """Writes k, v (bf16 [T, heads_kv, d]) of one layer to the positions
         start[i], start[i] + 1, ... of slots[i]: one row per entry, or with
         cu_seqlens (int32 [n + 1]) rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1."""
-        n, bf16 = slots.shape[0], self._torch.bfloat16
+        n, bf16, index = slots.numel(), self._bf16, self._index
         shape = k.shape
-        if len(shape) != 3 or shape[1:] != self._row or v.shape != shape:
+        if (len(shape) != 3 or shape[1] != self.heads_kv or shape[2] != self.head_dim
+                or v.shape != shape):
             raise ValueError(f"k, v: [T, {self.heads_kv}, {self.head_dim}] of one shape are expected")
         sk, sv = k.stride(), v.stride()
-        if (k.dtype is not bf16 or v.dtype is not bf16 or k.get_device() != self._index
-                or v.get_device() != self._index or sk[2] != 1 or sv[2] != 1):
+        if (k.dtype is not bf16 or v.dtype is not bf16 or k.get_device() != index
+                or v.get_device() != index or sk[2] != 1 or sv[2] != 1):
             raise ValueError("k, v: bfloat16 on the cache's device, d contiguous, are expected")
         if cu_seqlens is None and shape[0] != n:
             raise ValueError("write: one row per slot is expected without cu_seqlens")
@@ -127,27 +137,24 @@ class PagedCache:
         its slot (slots int32 [B]; None: slot b for query b), with a window and
         first tokens as in forward_general.  The newest token has to be in the
         cache.  LSE: fp32 [B, H]."""
-        torch = self._torch
-        shape, sq = q.shape, q.stride()
+        shape = q.shape
         if len(shape) != 3 or shape[2] != self.head_dim:
             raise ValueError(f"q: [B, H, {self.head_dim}] is expected")
         B, H, d = shape
         if H < 1 or H % self.heads_kv:
             raise ValueError("q's heads must be a multiple of the cache's")
+        sq = self._queries("q", q, shape)
         if out is None:
-            out = q.new_empty(shape)
-        so = out.stride()
+            out = self._torch.empty_like(q)
+            so = out.stride()
+        else:
+            so = self._queries("out", out, shape)
         if lse is None:
-            lse = q.new_empty((B, H), dtype=torch.float32)
-        elif (lse.shape != (B, H) or lse.dtype is not torch.float32 or lse.get_device() != self._index
-              or not lse.is_contiguous()):
+            lse = q.new_empty((B, H), dtype=self._torch.float32)
+        elif (lse.shape != (B, H) or lse.dtype is not self._torch.float32
+              or lse.get_device() != self._index or not lse.is_contiguous()):
             raise ValueError(f"lse: contiguous float32 {(B, H)} on the cache's device is expected")
-        for name, t, st in (("q", q, sq), ("out", out, so)):
-            if (t.dtype is not torch.bfloat16 or t.get_device() != self._index or t.shape != shape
-                    or st[2] != 1):
-                raise ValueError(f"{name}: bfloat16 {tuple(shape)} on the cache's device, d "
-                                 "contiguous, is expected")
-        window, sinks = _fa._window(window, sinks)
+        window, sinks = _fa._window(window, sinks) if window or sinks else (0, 0)
         key = (B, H, window, sinks)
         size = self._sizes.get(key)
         if size is None:  # a function of the cache's sizes and these alone
@@ -163,7 +170,7 @@ class PagedCache:
     @_fa._nvtx("fa.cache.fork")
     def fork(self, src, dst):
         """Slot dst[i] lets its pages go and shares src[i]'s (fa_cache_fork)."""
-        n = src.shape[0]
+        n = src.numel()
         ws, size = self._workspace(n)
         self._call(self._lib.fa_cache_fork, self._ints("src", src, n), self._ints("dst", dst, n), n,
                    ws.data_ptr(), size)
@@ -171,7 +178,7 @@ class PagedCache:
     @_fa._nvtx("fa.cache.free")
     def free(self, slots):
         """The slots let their pages go and become empty."""
-        n = slots.shape[0]
+        n = slots.numel()
         self._call(self._lib.fa_cache_free, self._ints("slots", slots, n), n)
 
     @_fa._nvtx("fa.cache.compact")
@@ -189,7 +196,7 @@ class PagedCache:
         dst[i], every layer; the book-keeping stays (fa_cache_copy_pages)."""
         if source is not None and source.device != self.device:
             raise ValueError("copy_pages: both caches on one device are expected")
-        n = src.shape[0]
+        n = src.numel()
         ws, size = self._workspace(n)
         self._call(self._lib.fa_cache_copy_pages, None if source is None else source._ref,
                    self._ints("src", src, n), self._ints("dst", dst, n), n, ws.data_ptr(), size)
