@@ -213,10 +213,13 @@ __device__ __forceinline__ int tiles_of(const AttendParams& p, int b, int* slot,
 // What a row of that many tiles takes up in the shares.
 __device__ __forceinline__ uint32_t span_of(int tiles) { return tiles > 0 ? tiles + kRowCost : 0; }
 
-// The sequences that a block looks at together, in shared memory.
+// The sequences that a block looks at together, in shared memory: four a thread
+// (with one a thread, 256 ragged sequences took 71 us where these take 59).
+constexpr int kSeqsPerThread = 4, kSeqs = kThreads * kSeqsPerThread;
+
 struct Seqs {
-  int len[kThreads], tiles[kThreads], slot[kThreads];
-  uint32_t upto[kThreads];  // running sum of spans
+  int len[kSeqs], tiles[kSeqs], slot[kSeqs];
+  uint32_t upto[kSeqs];  // running sum of spans
   uint32_t scan[kWarps];
 };
 
@@ -243,16 +246,22 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   const int rows_per_seq = p.c.heads_kv * p.head_blocks;
 
   // ---- the shares: tiles of every sequence, their sum and this warp's part
-  auto load_seq = [&](int b) -> uint32_t {  // sequence b, this thread's
-    int n = 0, slot = -1, tiles = 0;
-    if (b < p.batch) tiles = tiles_of<KT>(p, b, &slot, &n);
-    sq.len[threadIdx.x] = n;
-    sq.slot[threadIdx.x] = slot;
-    sq.tiles[threadIdx.x] = tiles;
-    return span_of(tiles);
-  };
-  // inclusive prefix sum over the block into sq.upto; returns the sum of all
-  auto scan = [&](uint32_t x) -> uint32_t {
+  // Loads the sequences from b0 on and the running sums of their spans; returns
+  // the sum of all.
+  auto load_seqs = [&](int b0) -> uint32_t {
+    uint32_t upto[kSeqsPerThread], x = 0;
+    const int j0 = threadIdx.x * kSeqsPerThread;
+#pragma unroll
+    for (int i = 0; i < kSeqsPerThread; ++i) {
+      int n = 0, slot = -1, tiles = 0;
+      if (b0 + j0 + i < p.batch) tiles = tiles_of<KT>(p, b0 + j0 + i, &slot, &n);
+      sq.len[j0 + i] = n;
+      sq.slot[j0 + i] = slot;
+      sq.tiles[j0 + i] = tiles;
+      x += span_of(tiles);
+      upto[i] = x;
+    }
+    const uint32_t own = x;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
@@ -260,13 +269,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
     }
     if (lane == 31) sq.scan[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    uint32_t before = x - own, all = 0;
 #pragma unroll
     for (uint32_t w = 0; w < kWarps; ++w) {
       if (w < warp) before += sq.scan[w];
       all += sq.scan[w];
     }
-    sq.upto[threadIdx.x] = x + before;
+#pragma unroll
+    for (int i = 0; i < kSeqsPerThread; ++i) sq.upto[j0 + i] = before + upto[i];
     __syncthreads();
     return all;
   };
@@ -703,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
         }
         cluster_sync();  // nobody leaves while the others still read
       }
-      if (p.batch > kThreads) {
+      if (p.batch > kSeqs) {
         __syncthreads();
         if (p.c.d < D)  // the ring held fp32 sums
           for (uint32_t x = lane; x < C::WARP / 16; x += 32) st_shared_v4(ring + 16 * x, 0u, 0u, 0u, 0u);
@@ -729,8 +739,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   }
 
   uint32_t sum = 0, part = 0;  // spans of one row per sequence
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    part = scan(load_seq(b0 + threadIdx.x));
+  for (int b0 = 0; b0 < p.batch; b0 += kSeqs) {
+    part = load_seqs(b0);
     sum += part;
   }
   const uint32_t W = sum * rows_per_seq;
@@ -750,18 +760,20 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   blk_hi = full ? sh.begin(blk0 + kWarps) : 0;
 
   uint32_t chunk_lo = 0;  // tile at which this chunk of sequences begins
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    if (p.batch > kThreads) part = scan(load_seq(b0 + threadIdx.x));  // else it is still there
+  for (int b0 = 0; b0 < p.batch; b0 += kSeqs) {
+    if (p.batch > kSeqs) part = load_seqs(b0);  // else they are still there
     // rows without keys belong to no share: the last block's warps write theirs
     if (blockIdx.x == gridDim.x - 1) {
-      uint32_t none = __ballot_sync(0xffffffffu, b0 + static_cast<int>(threadIdx.x) < p.batch &&
-                                                     sq.tiles[threadIdx.x] == 0);
-      for (; none != 0u; none &= none - 1u) {
-        const int b = b0 + 32 * warp + __ffs(none) - 1;
-        for (int x = lane; x < p.heads * (p.c.d / 8); x += 32) {
-          const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
-          *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
-          if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
+      for (int i = 0; i < kSeqsPerThread; ++i) {
+        const int j = threadIdx.x * kSeqsPerThread + i;
+        uint32_t none = __ballot_sync(0xffffffffu, b0 + j < p.batch && sq.tiles[j] == 0);
+        for (; none != 0u; none &= none - 1u) {
+          const int b = b0 + static_cast<int>(32 * warp + __ffs(none) - 1) * kSeqsPerThread + i;
+          for (int x = lane; x < p.heads * (p.c.d / 8); x += 32) {
+            const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
+            *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
+            if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
+          }
         }
       }
     }
@@ -773,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
       Cursor at;
       {
         const uint32_t fs = (from - chunk_lo) / rows_per_seq;
-        int a = 0, z = kThreads - 1;
+        int a = 0, z = min(kSeqs, p.batch - b0) - 1;
         while (a < z) {
           const int mid = (a + z) / 2;
           if (sq.upto[mid] > fs) z = mid;
@@ -799,12 +811,13 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
       walk(b0, at, end, step, block_row);
     }
     chunk_lo = chunk_hi;
-    if (p.batch > kThreads) __syncthreads();  // the next chunk overwrites the sequences
+    if (p.batch > kSeqs) __syncthreads();  // the next chunk overwrites the sequences
   }
 }
 
-// Joins the parts of rows that were cut: a block per (row, up to 4 of its query
-// heads).  First the maximum and row sum of all parts' statistics at once, then
+// Joins the parts of rows that were cut: a block per (row, kJoinHeads of its query
+// heads), one head where there are few rows, which then have many parts (one row
+// of 100000 keys, 8 heads: 43 us with four heads a block, 26 with one).  First the maximum and row sum of all parts' statistics at once, then
 // the weighted sums: D / 8 threads over a head's columns, the others over the
 // parts, whose loads wait for nothing (with the maximum carried from part to
 // part, 16 rows of 37 parts at d = 256 took 13 us).  Which rows were cut, and
@@ -812,9 +825,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
 // for the attention kernel (which starts its dependents only once the kernels
 // before it are done): small enough to be resident beside it, a block goes
 // on at once when it ends.
-constexpr int kJoinThreads = 256, kJoinHeads = 4;
+constexpr int kJoinThreads = 256;
 
-template <int D, int KT>
+template <int D, int KT, int kJoinHeads>
 __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParams p) {
   constexpr int TPR = D / 8, GROUPS = kJoinThreads / (TPR * kJoinHeads), kJoinWarps = kJoinThreads / 32;
   __shared__ uint2 seqs[kJoinWarps];
@@ -824,6 +837,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
   const int b = blockIdx.x / rows_per_seq, rs = blockIdx.x - b * rows_per_seq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint2 sum = make_uint2(0u, 0u);  // spans of all sequences, and of those before b
+#pragma unroll 4
   for (int i = threadIdx.x; i < p.batch; i += kJoinThreads) {
     int slot, len;
     const uint32_t span = span_of(tiles_of<KT>(p, i, &slot, &len));
@@ -978,6 +992,15 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   return p;
 }
 
+template <int D, int KT, int JH>
+cudaError_t launch_join(const AttendParams& p, cudaStream_t stream) {
+  const int heads = p.group < p.block_heads ? p.group : p.block_heads;  // of a row
+  return launch_overlapped(join_kernel<D, KT, JH>,
+                           dim3(static_cast<unsigned>(p.batch * p.c.heads_kv * p.head_blocks),
+                                static_cast<unsigned>((heads + JH - 1) / JH)),
+                           dim3(kJoinThreads), 0, stream, p);
+}
+
 template <int D, int NB>
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t stream) {
   using C = DecodeCfg<D, NB>;
@@ -1023,10 +1046,9 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
   cudaError_t r = launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), dim3(kThreads), C::SMEM,
                                     stream, a);
   if (r == cudaSuccess && plan.cut)
-    r = launch_overlapped(join_kernel<D, C::KT>,
-                          dim3(static_cast<unsigned>(p.batch * p.c.heads_kv * p.head_blocks),
-                               static_cast<unsigned>(((p.group < p.block_heads ? p.group : p.block_heads) + kJoinHeads - 1) / kJoinHeads)),
-                          dim3(kJoinThreads), 0, stream, a);
+    r = p.batch * p.c.heads_kv * p.head_blocks * p.block_heads <= 4 * 148
+            ? launch_join<D, C::KT, 1>(a, stream)
+            : launch_join<D, C::KT, 4>(a, stream);
   return r;
 }
 

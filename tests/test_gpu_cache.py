@@ -454,7 +454,7 @@ def test_empty_calls(lib):
 
 
 @pytest.mark.parametrize("B,P,H,Hkv,d,window,sinks", [
-    (300, 16, 8, 2, 96, 0, 0), (130, 8, 20, 1, 64, 50, 3), (257, 4, 2, 2, 256, 0, 0), (1000, 16, 4, 1, 128, 0, 0)])
+    (300, 16, 8, 2, 96, 0, 0), (700, 16, 4, 1, 96, 0, 0), (1100, 16, 2, 1, 32, 9, 2), (130, 8, 20, 1, 64, 50, 3), (257, 4, 2, 2, 256, 0, 0), (1000, 16, 4, 1, 128, 0, 0)])
 def test_attend_many_sequences(lib, B, P, H, Hkv, d, window, sinks):
     """More sequences than a block looks at together: short, empty and one long one among them."""
     r = random.Random(B)
