@@ -759,38 +759,70 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   blk_lo = full ? sh.begin(blk0) : 0;
   blk_hi = full ? sh.begin(blk0 + kWarps) : 0;
 
-  uint32_t chunk_lo = 0;  // tile at which this chunk of sequences begins
-  for (int b0 = 0; b0 < p.batch; b0 += kSeqs) {
-    if (p.batch > kSeqs) part = load_seqs(b0);  // else they are still there
-    // rows without keys belong to no share: the last block's warps write theirs
-    if (blockIdx.x == gridDim.x - 1) {
-      for (int i = 0; i < kSeqsPerThread; ++i) {
-        const int j = threadIdx.x * kSeqsPerThread + i;
-        uint32_t none = __ballot_sync(0xffffffffu, b0 + j < p.batch && sq.tiles[j] == 0);
-        for (; none != 0u; none &= none - 1u) {
-          const int b = b0 + static_cast<int>(32 * warp + __ffs(none) - 1) * kSeqsPerThread + i;
-          for (int x = lane; x < p.heads * (p.c.d / 8); x += 32) {
-            const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
-            *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
-            if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
-          }
+  // the sequence of tile f of the chunk that begins at tile lo with sequence b0:
+  // the first whose running sum passes it
+  auto seq_at = [&](uint32_t f, uint32_t chunk, int b0) -> int {
+    const uint32_t fs = (f - chunk) / rows_per_seq;
+    int a = 0, z = min(kSeqs, p.batch - b0) - 1;
+    while (a < z) {
+      const int mid = (a + z) / 2;
+      if (sq.upto[mid] > fs) z = mid;
+      else a = mid + 1;
+    }
+    return a;
+  };
+  // rows without keys belong to no share: the last block's warps write theirs
+  auto write_empty = [&](int b0) {
+    if (blockIdx.x != grid - 1) return;
+    for (int i = 0; i < kSeqsPerThread; ++i) {
+      const int j = threadIdx.x * kSeqsPerThread + i;
+      uint32_t none = __ballot_sync(0xffffffffu, b0 + j < p.batch && sq.tiles[j] == 0);
+      for (; none != 0u; none &= none - 1u) {
+        const int b = b0 + static_cast<int>(32 * warp + __ffs(none) - 1) * kSeqsPerThread + i;
+        for (int x = lane; x < p.heads * (p.c.d / 8); x += 32) {
+          const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
+          *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
+          if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
         }
       }
     }
+  };
+
+  // The sequences that the block looks at begin with the one of its first share
+  // (begun at a multiple of kSeqs instead, the warps of one block that lay on both
+  // sides of such a place waited for one another and ended last, twice as late)
+  const uint32_t blk_from = blk0 < sh.n ? sh.begin(blk0) : W;
+  const uint32_t blk_end = blk0 < sh.n ? sh.begin(min(blk0 + active, sh.n)) : W;
+  uint32_t chunk_lo = 0;  // tile at which the chunk of sequences begins
+  int b_from = 0;
+  if (p.batch > kSeqs) {
+    uint32_t from_lo = W;
+    for (int b0 = 0; b0 < p.batch; b0 += kSeqs) {
+      part = load_seqs(b0);
+      write_empty(b0);
+      const uint32_t next_lo = chunk_lo + part * rows_per_seq;
+      if (blk_from >= chunk_lo && blk_from < next_lo) {
+        const int j = seq_at(blk_from, chunk_lo, b0);
+        b_from = b0 + j;
+        from_lo = chunk_lo + (sq.upto[j] - span_of(sq.tiles[j])) * rows_per_seq;
+      }
+      chunk_lo = next_lo;
+      __syncthreads();  // the next chunk overwrites the sequences
+    }
+    chunk_lo = from_lo;
+  } else {
+    write_empty(0);
+  }
+  for (int b0 = b_from; b0 < p.batch && chunk_lo < blk_end; b0 += kSeqs) {
+    if (p.batch > kSeqs) part = load_seqs(b0);  // else they are still there
     const uint32_t chunk_hi = chunk_lo + part * rows_per_seq;
     const uint32_t from = max(lo, chunk_lo);
     uint32_t end = min(hi, chunk_hi), step = 1;
     if (from < end) {
-      // the row of tile `from`: the first sequence whose running sum passes it
+      // the row of tile `from`
       Cursor at;
       {
-        const uint32_t fs = (from - chunk_lo) / rows_per_seq;
-        int a = 0, z = min(kSeqs, p.batch - b0) - 1;
-        while (a < z) {
-          const int mid = (a + z) / 2;
-          if (sq.upto[mid] > fs) z = mid;
-          else a = mid + 1;
-        }
+        const int a = seq_at(from, chunk_lo, b0);
         at.j = a;
         const uint32_t span = span_of(sq.tiles[a]);
         const uint32_t seq_lo = chunk_lo + (sq.upto[a] - span) * rows_per_seq;
