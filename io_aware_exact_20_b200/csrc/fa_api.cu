@@ -267,7 +267,11 @@ int64_t ws_rows(const Problem& p, int* npad, int64_t* rtot) {
 // Parts per backward unit under grouped K / V heads: the smallest divisor of
 // the group whose parts give about four units per SM of the 148 (every divisor
 // up to the whole group when there are fewer); 1 without grouping.  A split
-// unit adds its dK / dV into fp32 accumulators converted at the end.
+// unit adds its dK / dV into fp32 accumulators converted at the end.  Under a
+// window the units are equally long, so one and a half per SM balance them, and
+// short, so a part's set-up and fp32 slices weigh more (16K, 4 K / V heads of 4,
+// d = 128, window 1024: 607 us in 512 whole units, 705 in 1024 halves; 4K, window
+// 512: 135 us in 256 halves, 145 in 128 whole units, 169 in 512 quarters).
 std::atomic<int> g_gqa_split{0};  // test support: forced parts, 0 = automatic
 
 int split_of(const Problem& p) {
@@ -281,7 +285,7 @@ int split_of(const Problem& p) {
   for (int c = 1; c <= G; ++c) {
     if (G % c) continue;
     s = c;
-    if (units * c >= 4 * 148) break;
+    if (units * c >= (p.window > 0 ? 3 * 148 / 2 : 4 * 148)) break;
   }
   return s;
 }
