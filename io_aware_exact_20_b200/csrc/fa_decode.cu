@@ -911,6 +911,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
   if (active != kWarps || first >= last) first = last = c1 + 1;
   const uint32_t n1 = first - c0, n2 = n1 + (last - first) / kWarps;
   const uint32_t parts = n2 + c1 + 1 - last;
+  if (parts == 1) return;  // one block's shares were the whole row: written already
   auto share_at = [&](uint32_t i) {
     return i < n1 ? c0 + i : i < n2 ? first + (i - n1) * kWarps : last + (i - n2);
   };

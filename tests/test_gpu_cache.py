@@ -557,3 +557,17 @@ def test_attend_into_its_own_queries(lib):
         want = cache.attend(0, q)
         cache.attend(0, q, out=q)
         assert torch.equal(q, want[0])
+
+
+@pytest.mark.parametrize("B,Hkv,G,d,lo,hi,seed", [
+    (70, 2, 8, 128, 159, 713, 1), (28, 8, 4, 256, 1, 416, 2), (76, 2, 1, 256, 18, 646, 3), (17, 8, 2, 256, 1, 397, 4),
+    (150, 4, 4, 64, 100, 900, 5), (64, 4, 4, 128, 190, 210, 6), (90, 4, 2, 128, 320, 320, 7), (148, 4, 1, 128, 96, 96, 8)])
+def test_attend_rows_and_shares_of_like_length(lib, B, Hkv, G, d, lo, hi, seed):
+    """Shares of a few tiles against rows of a few dozen: rows that begin or end
+    with a share or a block, or fill one block exactly."""
+    r = random.Random(seed)
+    lens = [r.randint(lo, hi) for _ in range(B)]
+    cache = widened(lib, filled(lib, lens, 16, Hkv, d, seed=seed))
+    q = randn((B, Hkv * G, d), 68)
+    o, lse = cache.attend(0, q)
+    check_attend(cache, 0, q, None, o, lse, d ** -0.5)
