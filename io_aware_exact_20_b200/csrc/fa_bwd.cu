@@ -1224,6 +1224,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       const bool row_ok = jg < w.lk;
       const long long kr = w.krow + jg;
+      // Windowed units are short, so their epilogue weighs: a row's pieces are
+      // stored by neighbouring lanes, whole sectors an instruction (a thread per row
+      // stored half sectors of 32 rows: 4.2 us a unit at d = 128, 2 so; 16 heads of 16K,
+      // window 128: 300 us, 268 so)
+      constexpr bool kStaged = WIN;
+      constexpr int kPieces = L::HD / 16;         // 16-byte pieces of a row of this warp's columns
+      constexpr uint32_t kRowBytes = 16 * kPieces;
+      const uint32_t stage0 = sbase + L::OFF_K + static_cast<uint32_t>(warp - 4) * 64u * kRowBytes;
+      auto stage_at = [&](int row, int piece) -> uint32_t {
+        const int x = kPieces == 8 ? row & 7 : (row >> 1) & 3;
+        return stage0 + row * kRowBytes + ((piece ^ x) << 4);
+      };
 #pragma unroll
       for (int c = 0; c < L::HD / 64; ++c) {
         const int tcol = wg * (L::HD / 2) + 32 * c;  // TMEM column of this CTA's slice
@@ -1266,6 +1278,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                    __uint_as_float(bk[4 * k + 3]) * sc);
             }
           }
+        } else if constexpr (kStaged) {
+          // this warp's 32 rows x HD / 2 columns of dV, then of dK, in the K / V
+          // tiles' shared memory (their MMAs are done), 16-byte pieces swizzled
+          // by the row
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t vv[4], kk4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = 8 * k + 2 * e;
+              vv[e] = pack_bf16(__uint_as_float(a[x]) * p.drop_rscale,
+                                __uint_as_float(a[x + 1]) * p.drop_rscale);
+              kk4[e] = pack_bf16(__uint_as_float(bk[x]) * p.scale, __uint_as_float(bk[x + 1]) * p.scale);
+            }
+            const uint32_t at = stage_at(lane, 4 * c + k);
+            st_shared_v4(at, vv[0], vv[1], vv[2], vv[3]);
+            st_shared_v4(at + 32 * kRowBytes, kk4[0], kk4[1], kk4[2], kk4[3]);
+          }
         } else if (row_ok && col < p.d_real && FA_IN_BOUNDS(p.status, dv_off, 32, p.ext.dv) &&
                    FA_IN_BOUNDS(p.status, dk_off, 32, p.ext.dk)) {
           uint4* dvp = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + dv_off);
@@ -1282,6 +1312,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             dvp[k] = make_uint4(vv[0], vv[1], vv[2], vv[3]);
             dkp[k] = make_uint4(kk4[0], kk4[1], kk4[2], kk4[3]);
+          }
+        }
+      }
+      if (kStaged && !(GEN && (S > 1 || (WIN && w.kb < p.sink_tiles)))) {
+        __syncwarp();
+        constexpr int kRows = 32 / kPieces;  // rows of a store instruction
+        const int piece = lane % kPieces;
+        const int col = L::HD * hf + wg * (L::HD / 2) + 8 * piece;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kRows) {
+          const int row = r0 + lane / kPieces;
+          const int key = w.kb * 128 + wq * 32 + row;
+          const long long r = w.krow + key;
+          const long long dv_off = w.tb * p.sdv.b + w.hk * p.sdv.h + r * p.sdv.r + col;
+          const long long dk_off = w.tb * p.sdk.b + w.hk * p.sdk.h + r * p.sdk.r + col;
+          if (key < w.lk && col < p.d_real && FA_IN_BOUNDS(p.status, dv_off, 8, p.ext.dv) &&
+              FA_IN_BOUNDS(p.status, dk_off, 8, p.ext.dk)) {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + dv_off) =
+                ld_shared_v4(stage_at(row, piece));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + dk_off) =
+                ld_shared_v4(stage_at(row, piece) + 32 * kRowBytes);
           }
         }
       }
