@@ -177,14 +177,15 @@ __device__ __forceinline__ Visible visible_of(int n, int window, int sinks) {
 }
 
 // Eight columns of query head h of sequence b: O = out / sum, LSE = ln2 (m + log2 sum).
+// A sum of zero is a row that sees nothing (0, -inf); one that is not a number stays so in both.
 __device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, int col, float m, float sum,
                                           const float (&out)[8]) {
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) =
       make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
                  pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
   if (col == 0)
-    p.lse[static_cast<long long>(b) * p.heads + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[static_cast<long long>(b) * p.heads + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // out += f * eight consecutive sums
@@ -223,7 +224,8 @@ struct Seqs {
   uint32_t scan[kWarps];
 };
 
-// A place in the walk: tile f of the row that has tiles [lo, hi) of the batch's, row rs (K / V head hk, block of heads) of sequence j of the chunk.
+// A place in the walk: tile f of the row that has tiles [lo, hi) of the batch's,
+// row rs (K / V head hk, block of heads) of sequence j of the chunk.
 struct Cursor {
   uint32_t f, lo, hi;
   int j, rs, hk;
@@ -579,12 +581,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             l[nb][u] = sum_rows(l[nb][u]);
-            inv[u] = l[nb][u] > 0.f ? 1.f / l[nb][u] : 0.f;
+            inv[u] = l[nb][u] == 0.f ? 0.f : 1.f / l[nb][u];
             const int h = 8 * nb + 2 * q4 + u;
             if (g == 0 && h < hn) {
               if (whole)
                 p.lse[static_cast<long long>(b) * p.heads + h0 + h] =
-                    l[nb][u] > 0.f ? (m[nb][u] + log2f(l[nb][u])) * kLn2 : -INFINITY;
+                    l[nb][u] == 0.f ? -INFINITY : (m[nb][u] + log2f(l[nb][u])) * kLn2;
               else
                 p.part_stat[pr + h] = make_float2(m[nb][u], l[nb][u]);
             }
@@ -849,14 +851,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
 
 // Joins the parts of rows that were cut: a block per (row, kJoinHeads of its query
 // heads), one head where there are few rows, which then have many parts (one row
-// of 100000 keys, 8 heads: 43 us with four heads a block, 26 with one).  First the maximum and row sum of all parts' statistics at once, then
-// the weighted sums: D / 8 threads over a head's columns, the others over the
-// parts, whose loads wait for nothing (with the maximum carried from part to
-// part, 16 rows of 37 parts at d = 256 took 13 us).  Which rows were cut, and
-// where, follows from the lengths alone, so all of that happens before the wait
-// for the attention kernel (which starts its dependents only once the kernels
-// before it are done): small enough to be resident beside it, a block goes
-// on at once when it ends.
+// of 100000 keys, 8 heads: 43 us with four heads a block, 26 with one).  First
+// the maximum and row sum of all parts' statistics at once, then the weighted
+// sums: D / 8 threads over a head's columns, the others over the parts, whose
+// loads wait for nothing (with the maximum carried from part to part, 16 rows of
+// 37 parts at d = 256 took 13 us).  Which rows were cut, and where, follows from
+// the lengths alone, so all of that happens before the wait for the attention
+// kernel (which starts its dependents only once the kernels before it are done):
+// small enough to be resident beside it, a block goes on at once when it ends.
 constexpr int kJoinThreads = 256;
 
 template <int D, int KT, int kJoinHeads>

@@ -306,6 +306,31 @@ def test_attend_large_scores(lib):
         plain64.check("o", o[b], r["o"], r["o_tol"] + 1e-3 * v[0].abs().max())
 
 
+@pytest.mark.parametrize("lens,H,Hkv,d", [
+    ([60, 33, 1], 4, 2, 128),             # a cluster of blocks per row
+    ([60] * 300 + [7], 4, 2, 64),         # rows whole in a share
+    ([40000, 500, 9000, 3], 8, 2, 128),   # rows cut, and joined
+    ([900] * 80, 16, 1, 256),
+])
+def test_attend_keeps_what_is_not_a_number(lib, lens, H, Hkv, d):
+    """A visible key, or a query, that is not a number: O and LSE of the rows that
+    see it are none either, and every other row is as it was."""
+    cache = filled(lib, lens, 32, Hkv, d, seed=9)
+    q = randn((len(lens), H, d), 64)
+    o, lse = cache.attend(0, q)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    bad = torch.zeros(len(lens), H, dtype=torch.bool, device="cuda")
+    for s in {0, len(lens) // 2}:  # the last token of K / V head 0
+        at = lens[s] - 1
+        cache.k[0, cache.table[s, at // 32], 0, at % 32, 5] = float("nan")
+        bad[s, :H // Hkv] = True
+    q[-1, -1, d - 1] = float("nan")
+    bad[-1, -1] = True
+    o1, lse1 = cache.attend(0, q)
+    assert o1[bad].isnan().all() and lse1[bad].isnan().all()
+    assert torch.equal(o1[~bad], o[~bad]) and torch.equal(lse1[~bad], lse[~bad])
+
+
 def test_offsets_beyond_32_bits(lib):
     """Pages past 2^32 bytes and past 2^31 elements of the pool."""
     P, d, pages = 256, 128, 70000
