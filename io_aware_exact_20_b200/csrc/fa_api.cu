@@ -81,6 +81,7 @@ struct Problem {
   int64_t drop_row0, drop_key0;  // dropout positions of the first query row and key
   int Hkv;                       // K / V heads (H / Hkv query heads share each)
   int window, sinks;             // sliding window (0: none), first keys that stay visible
+  bool own_key;                  // the call's window is the query's own key alone
 
   int rows_q() const { return packed ? total_q : nq; }
   int rows_k() const { return packed ? total_k : nk; }
@@ -147,6 +148,7 @@ fa_status_t resolve(const fa_attention_desc_t* a, Problem* p, Uses uses) {
   // Positions are below kMaxRows, so longer windows and more first keys than
   // that change nothing either (and the kernels' sums stay inside 32 bits).
   p->window = a->window < a->seqlen_k ? a->window : 0;
+  p->own_key = a->window == 1 && a->sinks == 0;  // (of one key, too)
   p->sinks = a->sinks < kMaxRows ? a->sinks : kMaxRows;
   p->drop_row0 = a->dropout_row0;
   p->drop_key0 = a->dropout_key0;
@@ -463,8 +465,7 @@ fa_status_t bwd_params(fa::BwdParams* p, const Problem& pr, const void* workspac
   // A window of the query's own key alone: its probability is 1 whatever the
   // score, so dQ and dK are exactly 0; dP - D would leave rounding noise there.
   // (This scale is only the final factor of dQ and dK.)
-  const bool own_key_only = pr.window == 1 && pr.sinks == 0;
-  p->scale = own_key_only ? 0.f : pr.scale;
+  p->scale = pr.own_key ? 0.f : pr.scale;
   p->scale_log2 = static_cast<float>(static_cast<double>(pr.scale) * kLog2e);
   p->causal = pr.causal;
   // the main kernel's units are (b, K / V head, key tile): its head groups are

@@ -1,0 +1,29 @@
+"""Sliding window at the ends of its range: one key, pieces of the first keys'
+walks together with every other mask and layout, replayed graphs."""
+
+import pytest
+import torch
+
+import plain64
+from test_gpu_window import randn, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("layout,B,H,Hkv,d,p", [("bhsd", 2, 4, 2, 64, 0.0), ("bhsd", 3, 2, 2, 128, 0.0),
+                                                ("bshd", 2, 4, 1, 128, 0.3), ("bhsd", 2, 2, 1, 256, 0.0),
+                                                ("thd", 5, 4, 2, 64, 0.0), ("thd", 4, 2, 1, 128, 0.25)])
+def test_own_key_alone_of_one_key(lib, layout, B, H, Hkv, d, p):
+    """Window 1 without first tokens over sequences of one key: that key has
+    probability 1 whatever the score, so dQ and dK are exactly zero here too."""
+    shape = {"bhsd": lambda h: (B, h, 1, d), "bshd": lambda h: (B, 1, h, d), "thd": lambda h: (B, h, d)}[layout]
+    q, do, k, v = randn(shape(H), 1), randn(shape(H), 2), randn(shape(Hkv), 3), randn(shape(Hkv), 4)
+    kw = dict(layout=layout, causal=True, window=1, dropout_p=p, seed=5)
+    if layout == "thd":
+        cu = list(range(B + 1))
+        kw.update(cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=1, max_seqlen_k=1)
+    got = run(lib, q, k, v, do, **kw)
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+    if not p:
+        heads = {"bhsd": 1, "bshd": 2, "thd": 1}[layout]
+        assert torch.equal(got["o"], v.repeat_interleave(H // Hkv, heads))
