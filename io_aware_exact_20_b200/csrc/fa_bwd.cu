@@ -402,11 +402,10 @@ __device__ __forceinline__ void post_sink(const BwdParams& p, int bx, int bh) {
   cvt(p.ws_sv + acc, static_cast<__nv_bfloat16*>(p.dv) + dv_off);
 }
 
-// All conversions in one launch: dQ's blocks, then those of the split units'
-// dK / dV, then the first keys' (a launch each cost 3 us of latency and 2.4 us
-// of the host).
+// Several conversions in one launch: dQ's blocks (dq_x = 0: none), then those of
+// the split units' dK / dV, then the first keys'.
 template <int D>
-__global__ void __launch_bounds__(256, 4) bwd_post_all_kernel(const BwdParams p, int dq_x, int kv_x,
+__global__ void __launch_bounds__(256) bwd_post_all_kernel(const BwdParams p, int dq_x, int kv_x,
                                                              int sink_x) {
   griddep_wait();
   griddep_launch_dependents();
@@ -1480,21 +1479,36 @@ cudaError_t launch_main_t(const CUtensorMap& tq, const CUtensorMap& tk, const CU
 }
 
 template <int D>
+cudaError_t launch_post_t(const BwdParams& p, cudaStream_t stream) {
+  return launch_overlapped(bwd_post_kernel<D>, prepost_grid<D>(p), dim3(256), 0, stream, p);
+}
+
+// A small call's conversions go in one launch (a launch each cost 3 us of latency
+// and 2.4 us of the host); a large one's dQ has its own, whose blocks hold a third
+// of the registers and keep twice the loads in flight.  dQ and two slices of dK and
+// dV in two launches and in one, launch latency not counted: 16 heads of 16K over
+// 4, d = 128 (20480 blocks), 53 and 70 us; 8 heads of 8K over one, d = 256 (9216),
+// 37 and 47; 16 heads of 4K over one, d = 128 (4352), 23.5 and 26; 2 x 8 heads of
+// 4K over 2, d = 64 (2560), 14 and 13.6.
+constexpr long long kTogether = 4096;  // blocks
+
+template <int D>
 cudaError_t launch_post_all_t(const BwdParams& p, cudaStream_t stream) {
   const long long key_rows = (static_cast<long long>(p.rows.nk) + 127) / 128 * 128;
   const dim3 dq = prepost_grid<D>(p);
   const int kv_x = p.split > 1 ? static_cast<int>(key_rows / kRowsPerBlock<D>) : 0;
   const int sink_x = 128 * p.sink_tiles / kRowsPerBlock<D>;
-  const long long blocks = static_cast<long long>(dq.x) * dq.y +
-                           static_cast<long long>(kv_x + sink_x) * p.B * (p.H / p.group);
+  const long long n_dq = static_cast<long long>(dq.x) * dq.y;
+  const long long n_kv = static_cast<long long>(kv_x + sink_x) * p.B * (p.H / p.group);
+  const bool together = n_dq + n_kv <= kTogether;
+  if (!together) {
+    const cudaError_t e = launch_post_t<D>(p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const long long blocks = together ? n_dq + n_kv : n_kv;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(bwd_post_all_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                           stream, p, static_cast<int>(dq.x), kv_x, sink_x);
-}
-
-template <int D>
-cudaError_t launch_post_t(const BwdParams& p, cudaStream_t stream) {
-  return launch_overlapped(bwd_post_kernel<D>, prepost_grid<D>(p), dim3(256), 0, stream, p);
+                           stream, p, together ? static_cast<int>(dq.x) : 0, kv_x, sink_x);
 }
 
 }  // namespace

@@ -27,3 +27,29 @@ def test_own_key_alone_of_one_key(lib, layout, B, H, Hkv, d, p):
     if not p:
         heads = {"bhsd": 1, "bshd": 2, "thd": 1}[layout]
         assert torch.equal(got["o"], v.repeat_interleave(H // Hkv, heads))
+
+
+@pytest.mark.parametrize("H,Hkv,N,d,window,sinks", [
+    (16, 1, 4200, 128, 300, 4),     # dQ converted by a launch of its own; first keys in pieces
+    (16, 2, 4200, 128, 200, 0),     # split units alone
+    (16, 1, 4200, 128, 0, 0),       # no window
+    (8, 1, 4300, 256, 130, 140),
+    (32, 4, 4099, 64, 600, 3),
+])
+def test_gradients_of_many_row_blocks(lib, H, Hkv, N, d, window, sinks):
+    """Grouped heads long enough that dQ is converted apart from dK and dV."""
+    q, do = randn((1, H, N, d), 11), randn((1, H, N, d), 12)
+    k, v = randn((1, Hkv, N, d), 13), randn((1, Hkv, N, d), 14)
+    got = run(lib, q, k, v, do, causal=True, window=window, sinks=sinks)
+    mask = plain64.visible(N, N, q.device, window=window, sinks=sinks)
+    G, kv = H // Hkv, {}
+    for h in range(H):
+        r = plain64.head(q[0, h].double(), k[0, h // G].double(), v[0, h // G].double(), d ** -0.5, mask, do[0, h].double())
+        plain64.check_lse(got["lse"][0, h], r["lse"])
+        for n in ("o", "dq"):
+            plain64.check(n, got[n][0, h], r[n], r[n + "_tol"])
+        for n in ("dk", "dk_tol", "dv", "dv_tol"):
+            kv[n] = kv[n] + r[n] if h % G else r[n]
+        if h % G == G - 1:
+            for n in ("dk", "dv"):  # (rounded once more, as plain64.padded says)
+                plain64.check(n, got[n][0, h // G], kv[n], kv[n + "_tol"] + plain64.BF16 * kv[n].abs())
