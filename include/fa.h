@@ -330,9 +330,9 @@ fa_status_t fa_qkv_projection(const void* x, const void* w, const void* bias, vo
  * the device.  They check these against the sizes given here: a slot outside
  * [0, slots) is skipped, a page outside [0, pages) holds no keys, a length
  * outside [0, max_pages * page_size] is cut to it.  Calls that change the same
- * cache are ordered by the caller (one stream, or events).  Workspaces:
- * fa_cache_workspace_size(cache, n) bytes, 256-byte aligned, contents
- * irrelevant, not shared by calls that may overlap. */
+ * cache are ordered by the caller (one stream, or events).  Workspaces: at
+ * least the call's own size below, 256-byte aligned, contents irrelevant, not
+ * shared by calls that may overlap. */
 typedef struct {
   int layers, pages, page_size, heads_kv, head_dim;
   int slots, max_pages;
@@ -345,8 +345,14 @@ typedef struct {
   int32_t* refs;
 } fa_cache_t;
 
-/* Workspace of fa_cache_extend, fa_cache_fork, fa_cache_copy_pages (n: their
- * entries) and fa_cache_compact (n ignored).  0 if the description is invalid. */
+/* Workspace bytes of each call (n: its entries), 0 if the description is
+ * invalid.  A fork saves the table rows of its sources (n * max_pages cells);
+ * the others need a few cells per entry and page. */
+size_t fa_cache_extend_workspace_size(const fa_cache_t* cache, int n);
+size_t fa_cache_fork_workspace_size(const fa_cache_t* cache, int n);
+size_t fa_cache_compact_workspace_size(const fa_cache_t* cache);
+size_t fa_cache_copy_pages_workspace_size(const fa_cache_t* cache, int n);
+/* Enough for any of the four: the largest of those sizes. */
 size_t fa_cache_workspace_size(const fa_cache_t* cache, int n);
 
 /* Grows slots[i] by tokens[i] >= 0 tokens, i < n: takes pages for the new

@@ -150,6 +150,10 @@ SIGNATURES = {
     "fa_debug_bounds_checking": (_i, []),
     "fa_debug_set_gqa_split": (None, [_i]),
     "fa_cache_workspace_size": (_sz, [_CP, _i]),
+    "fa_cache_extend_workspace_size": (_sz, [_CP, _i]),
+    "fa_cache_fork_workspace_size": (_sz, [_CP, _i]),
+    "fa_cache_compact_workspace_size": (_sz, [_CP]),
+    "fa_cache_copy_pages_workspace_size": (_sz, [_CP, _i]),
     "fa_cache_extend": (_i, [_CP, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
     "fa_cache_write": (_i, [_CP, _i, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i, _i, _vp]),
     "fa_cache_fork": (_i, [_CP, _vp, _vp, _i, _vp, _sz, _vp]),

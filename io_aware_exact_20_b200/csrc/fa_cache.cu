@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 
 #include <climits>
+#include <initializer_list>
 
 #include "cache.h"
 #include "kernels.h"
@@ -490,17 +491,19 @@ Moves carve_moves(Carve* w, int64_t n) {
   return m;
 }
 
-// the largest of the four calls' needs
-int64_t workspace_ints(const Cache& c, int n) {
-  const int64_t extend = 64 + 5 * round64(n) + round64(c.slots) + round64(c.pages);
-  const int64_t fork = round64(static_cast<int64_t>(n) * c.max_pages) + round64(n);
-  const int64_t compact = 64 + 4 * round64(c.pages);
-  int64_t x = extend > fork ? extend : fork;
-  return x > compact ? x : compact;
+// Each call's workspace.  Only a fork saves table rows: n * max_pages cells,
+// which the others' lists have no use for (65536 entries of 8192 pages: 2 GiB).
+int64_t moves_ints(int64_t n) { return 64 + 3 * round64(n); }
+int64_t extend_ints(const Cache& c, int n) {
+  return moves_ints(n) + 2 * round64(n) + round64(c.slots) + round64(c.pages);
 }
+int64_t fork_ints(const Cache& c, int n) {
+  return round64(n) + round64(static_cast<int64_t>(n) * c.max_pages);
+}
+int64_t compact_ints(const Cache& c) { return moves_ints(c.pages) + round64(c.pages); }
 
-bool workspace_ok(const Cache& c, int n, const void* ws, size_t bytes) {
-  return cache_aligned(ws, 256) && bytes >= static_cast<size_t>(workspace_ints(c, n)) * 4;
+bool workspace_ok(int64_t ints, const void* ws, size_t bytes) {
+  return cache_aligned(ws, 256) && bytes >= static_cast<size_t>(ints) * 4;
 }
 
 bool ints_ok(const void* p) { return cache_aligned(p, 4); }
@@ -520,10 +523,37 @@ fa_status_t done(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 
 extern "C" {
 
-size_t fa_cache_workspace_size(const fa_cache_t* cache, int n) {
+size_t fa_cache_extend_workspace_size(const fa_cache_t* cache, int n) {
   fa::Cache c;
   if (fa::cache_resolve(cache, false, &c) != FA_OK || n < 0) return 0;
-  return static_cast<size_t>(fa::workspace_ints(c, n)) * 4;
+  return static_cast<size_t>(fa::extend_ints(c, n)) * 4;
+}
+
+size_t fa_cache_fork_workspace_size(const fa_cache_t* cache, int n) {
+  fa::Cache c;
+  if (fa::cache_resolve(cache, false, &c) != FA_OK || n < 0) return 0;
+  return static_cast<size_t>(fa::fork_ints(c, n)) * 4;
+}
+
+size_t fa_cache_compact_workspace_size(const fa_cache_t* cache) {
+  fa::Cache c;
+  if (fa::cache_resolve(cache, false, &c) != FA_OK) return 0;
+  return static_cast<size_t>(fa::compact_ints(c)) * 4;
+}
+
+size_t fa_cache_copy_pages_workspace_size(const fa_cache_t* cache, int n) {
+  fa::Cache c;
+  if (fa::cache_resolve(cache, false, &c) != FA_OK || n < 0) return 0;
+  return static_cast<size_t>(fa::moves_ints(n)) * 4;
+}
+
+size_t fa_cache_workspace_size(const fa_cache_t* cache, int n) {
+  size_t most = 0;
+  for (const size_t x : {fa_cache_extend_workspace_size(cache, n), fa_cache_fork_workspace_size(cache, n),
+                         n < 0 ? size_t{0} : fa_cache_compact_workspace_size(cache),
+                         fa_cache_copy_pages_workspace_size(cache, n)})
+    most = x > most ? x : most;
+  return most;
 }
 
 fa_status_t fa_cache_extend(const fa_cache_t* cache, const int32_t* slots, const int32_t* tokens,
@@ -535,7 +565,7 @@ fa_status_t fa_cache_extend(const fa_cache_t* cache, const int32_t* slots, const
   if (n < 0) return FA_ERR_INVALID_ARG;
   if (n == 0) return FA_OK;
   if (!fa::ints_ok(slots) || !fa::ints_ok(tokens) || !fa::ints_ok(start)) return FA_ERR_INVALID_ARG;
-  if (!fa::workspace_ok(c, n, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  if (!fa::workspace_ok(fa::extend_ints(c, n), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};
   fa::ExtendWork w;
   w.moves = fa::carve_moves(&carve, n);
@@ -592,7 +622,7 @@ fa_status_t fa_cache_fork(const fa_cache_t* cache, const int32_t* src, const int
   if (n < 0) return FA_ERR_INVALID_ARG;
   if (n == 0) return FA_OK;
   if (!fa::ints_ok(src) || !fa::ints_ok(dst)) return FA_ERR_INVALID_ARG;
-  if (!fa::workspace_ok(c, n, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  if (!fa::workspace_ok(fa::fork_ints(c, n), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};
   fa::ForkWork w;
   w.lens = carve.take(n);
@@ -623,7 +653,7 @@ fa_status_t fa_cache_compact(const fa_cache_t* cache, int32_t* used, void* works
   const fa_status_t st = fa::cache_resolve(cache, true, &c);
   if (st != FA_OK) return st;
   if (!fa::ints_ok(used)) return FA_ERR_INVALID_ARG;
-  if (!fa::workspace_ok(c, 0, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  if (!fa::workspace_ok(fa::compact_ints(c), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};
   fa::CompactWork w;
   w.moves = fa::carve_moves(&carve, c.pages);
@@ -657,7 +687,7 @@ fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from,
     return FA_ERR_INVALID_ARG;
   if (n == 0) return FA_OK;
   if (!fa::ints_ok(src) || !fa::ints_ok(dst)) return FA_ERR_INVALID_ARG;
-  if (!fa::workspace_ok(to, n, workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
+  if (!fa::workspace_ok(fa::moves_ints(n), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};
   const fa::Moves m = fa::carve_moves(&carve, n);
   const bool same = of.k == to.k || of.v == to.v;

@@ -82,10 +82,11 @@ class PagedCache:
                              "is expected")
         return st
 
-    def _workspace(self, n):
-        size = self._sizes.get(n)
+    def _workspace(self, call, *n):
+        key = (call, *n)
+        size = self._sizes.get(key)
         if size is None:  # a function of the cache's sizes and n alone
-            size = self._sizes[n] = self._lib.fa_cache_workspace_size(self._ref, n)
+            size = self._sizes[key] = getattr(self._lib, f"fa_cache_{call}_workspace_size")(self._ref, *n)
         return self.lengths.new_empty(size // 4), size
 
     def _call(self, fn, *args):
@@ -105,7 +106,7 @@ class PagedCache:
         first new position, -1 where it was not granted (fa_cache_extend)."""
         n = slots.numel()
         start = self.lengths.new_empty(n)
-        ws, size = self._workspace(n)
+        ws, size = self._workspace("extend", n)
         self._call(self._lib.fa_cache_extend, self._ints("slots", slots, n),
                    self._ints("tokens", tokens, n), n, start.data_ptr(), ws.data_ptr(), size)
         return start
@@ -171,7 +172,7 @@ class PagedCache:
     def fork(self, src, dst):
         """Slot dst[i] lets its pages go and shares src[i]'s (fa_cache_fork)."""
         n = src.numel()
-        ws, size = self._workspace(n)
+        ws, size = self._workspace("fork", n)
         self._call(self._lib.fa_cache_fork, self._ints("src", src, n), self._ints("dst", dst, n), n,
                    ws.data_ptr(), size)
 
@@ -186,7 +187,7 @@ class PagedCache:
         """Moves the pages in use into the lowest numbers; returns how many there
         are (int32 [1], on the device)."""
         used = self.lengths.new_empty(1)
-        ws, size = self._workspace(0)
+        ws, size = self._workspace("compact")
         self._call(self._lib.fa_cache_compact, used.data_ptr(), ws.data_ptr(), size)
         return used
 
@@ -197,6 +198,6 @@ class PagedCache:
         if source is not None and source.device != self.device:
             raise ValueError("copy_pages: both caches on one device are expected")
         n = src.numel()
-        ws, size = self._workspace(n)
+        ws, size = self._workspace("copy_pages", n)
         self._call(self._lib.fa_cache_copy_pages, None if source is None else source._ref,
                    self._ints("src", src, n), self._ints("dst", dst, n), n, ws.data_ptr(), size)
