@@ -398,8 +398,11 @@ fa_status_t fa_cache_compact(const fa_cache_t* cache, int32_t* used, void* works
 /* Copies page src[i] of `from` (NULL: of `cache`) to page dst[i] of `cache`,
  * i < n, all layers; book-keeping is not touched.  Both caches have the same
  * layers, page_size, heads_kv and head_dim.  A pair is skipped if a page is
- * out of range, if an earlier pair has the same destination, or (within one
- * cache) if its destination is any pair's source. */
+ * out of range, if an earlier pair has the same destination, or if its
+ * destination is any pair's source: within one cache, or where the two are views
+ * of one pool with the same layer, head and row strides (their pages or layers
+ * apart, or every n-th page), in any layer.  Caches that share memory in another
+ * way, parts of pages, are not told apart. */
 fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from, const int32_t* src,
                                 const int32_t* dst, int n, void* workspace,
                                 size_t workspace_bytes, void* stream);

@@ -10,8 +10,10 @@
 // host never waits and the calls can be captured.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <climits>
 #include <initializer_list>
+#include <numeric>
 
 #include "cache.h"
 #include "kernels.h"
@@ -447,7 +449,16 @@ __global__ void __launch_bounds__(256) renumber_kernel(const Cache c, const int3
 // copy: which pairs are made
 // ---------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(256) copy_plan_kernel(int pages_from, int pages_to, bool same,
+// Where the two caches of a copy share memory, page for page: page s of the
+// source lies (in some layer) where page d of the destination does iff
+// by + s * from == d * to, in elements.
+struct Shared {
+  static constexpr int kMost = 16;
+  int n;
+  long long by[kMost], from[kMost], to[kMost];
+};
+
+__global__ void __launch_bounds__(256) copy_plan_kernel(int pages_from, int pages_to, const Shared sh,
                                                         const int32_t* src, const int32_t* dst,
                                                         int n, int page_size, const Moves m) {
   griddep_wait();
@@ -455,8 +466,12 @@ __global__ void __launch_bounds__(256) copy_plan_kernel(int pages_from, int page
   const int i = blockIdx.x;
   const int s = src[i], d = dst[i];
   bool skip = s < 0 || s >= pages_from || d < 0 || d >= pages_to;
-  for (int j = threadIdx.x; j < n; j += blockDim.x)
-    skip = skip || (j < i && dst[j] == d) || (same && src[j] == d);
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    skip = skip || (j < i && dst[j] == d);
+    const int o = src[j];
+    if (o >= 0 && o < pages_from)
+      for (int k = 0; k < sh.n; ++k) skip = skip || sh.by[k] + o * sh.from[k] == d * sh.to[k];
+  }
   skip = __syncthreads_or(skip);
   if (threadIdx.x == 0) {
     m.src[i] = s;
@@ -504,6 +519,47 @@ int64_t compact_ints(const Cache& c) { return moves_ints(c.pages) + round64(c.pa
 
 bool workspace_ok(int64_t ints, const void* ws, size_t bytes) {
   return cache_aligned(ws, 256) && bytes >= static_cast<size_t>(ints) * 4;
+}
+
+// The places at which K or V of `of` shares memory with K or V of `to`: views of
+// one pool, their pages or layers apart.  False if there are more of them than
+// fit (no such views of one pool are known).
+bool shared_of(const Cache& of, const Cache& to, Shared* sh) {
+  struct Part {
+    const void* base;
+    long long layer, page, head, row;
+  };
+  const Part f[2] = {{of.k, of.k_layer, of.k_page, of.k_head, of.k_row},
+                     {of.v, of.v_layer, of.v_page, of.v_head, of.v_row}};
+  const Part t[2] = {{to.k, to.k_layer, to.k_page, to.k_head, to.k_row},
+                     {to.v, to.v_layer, to.v_page, to.v_head, to.v_row}};
+  sh->n = 0;
+  for (const Part& a : f)
+    for (const Part& b : t) {
+      // other strides: not the same pages
+      if ((of.layers > 1 && a.layer != b.layer) || (of.heads_kv > 1 && a.head != b.head) ||
+          (of.page_size > 1 && a.row != b.row))
+        continue;
+      const long long pf = of.pages > 1 ? a.page : 0, pt = to.pages > 1 ? b.page : 0;
+      const long long apart = static_cast<long long>(reinterpret_cast<intptr_t>(a.base) -
+                                                     reinterpret_cast<intptr_t>(b.base)) / 2;
+      const long long low = -(of.pages - 1) * pf, high = (to.pages - 1) * pt;  // of `by`, below
+      const long long step = std::gcd(pf, pt);
+      long long l0 = 0, l1 = 0;  // layers of the source ahead of the destination's
+      if (of.layers > 1) {
+        l0 = std::max<long long>(-(of.layers - 1), (low - apart) / a.layer - 1);
+        l1 = std::min<long long>(of.layers - 1, (high - apart) / a.layer + 1);
+      }
+      for (long long l = l0; l <= l1; ++l) {
+        const long long by = apart + l * a.layer;
+        if (by < low || by > high || (step > 0 ? by % step : by) != 0) continue;
+        if (sh->n == Shared::kMost) return false;
+        sh->by[sh->n] = by;
+        sh->from[sh->n] = pf;
+        sh->to[sh->n++] = pt;
+      }
+    }
+  return true;
 }
 
 bool ints_ok(const void* p) { return cache_aligned(p, 4); }
@@ -690,10 +746,11 @@ fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from,
   if (!fa::workspace_ok(fa::moves_ints(n), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};
   const fa::Moves m = fa::carve_moves(&carve, n);
-  const bool same = of.k == to.k || of.v == to.v;
+  fa::Shared shared;
+  if (!fa::shared_of(of, to, &shared)) return FA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_overlapped(fa::copy_plan_kernel, dim3(static_cast<unsigned>(n)), dim3(256),
-                                        0, s, of.pages, to.pages, same, src, dst, n, to.page_size, m);
+                                        0, s, of.pages, to.pages, shared, src, dst, n, to.page_size, m);
   if (e == cudaSuccess)
     e = fa::launch_overlapped(fa::move_kernel, dim3(fa::move_blocks(to, n)), dim3(256), 0, s, of, to, m);
   return fa::done(e);
