@@ -20,8 +20,20 @@ class PagedCache:
     refs      int32 [pages]: slots that hold a page, 0: free
 
     The tensors stay the caller's (they may be views of one buffer) and are
-    changed in place; ``allocate`` makes an empty cache.  Slots are given as int32 device
+    changed in place; ``allocate`` makes an empty cache.  The library keeps their
+    addresses, so these attributes and the sizes cannot be set: other tensors are
+    another PagedCache.  Slots are given as int32 device
     tensors.  Calls on one cache have to be ordered: one stream, or events."""
+
+    _FIXED = frozenset(("k", "v", "table", "lengths", "refs", "layers", "pages", "heads_kv", "page_size",
+                        "head_dim", "slots", "max_pages", "device"))
+
+    def __setattr__(self, name, value):
+        # (the same tensor comes back from an in-place operator, `cache.lengths += 1`)
+        if name in self._FIXED and "_sizes" in self.__dict__ and value is not getattr(self, name):
+            raise AttributeError(f"PagedCache.{name} cannot be replaced: its address and sizes are the "
+                                 "library's already; make another PagedCache")
+        object.__setattr__(self, name, value)
 
     def __init__(self, k, v, table, lengths, refs):
         import torch

@@ -44,3 +44,20 @@ def test_workspace_sizes_of_bad_descriptions(lib):
     for name in SIZES:
         assert size_of(lib, name, bad, 2) == 0 and size_of(lib, name, desc(lib), -1) == 0
     assert lib.library().fa_cache_workspace_size(ctypes.byref(desc(lib)), -1) == 0
+
+
+def test_tensors_of_a_cache_cannot_be_replaced(lib):
+    """The library keeps the addresses, so an assignment it would not notice is refused; the same tensor
+    may come back from an in-place operator."""
+    import torch
+    cache = lib.PagedCache.__new__(lib.PagedCache)
+    cache.lengths = torch.zeros(3, dtype=torch.int32)
+    cache.pages = 4
+    cache._sizes = {}  # the description is made
+    with pytest.raises(AttributeError, match="cannot be replaced"):
+        cache.lengths = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(AttributeError, match="cannot be replaced"):
+        cache.pages = 5
+    cache.lengths += 1
+    cache.label = "a user's own attribute"
+    assert cache.lengths.tolist() == [1, 1, 1] and cache.pages == 4

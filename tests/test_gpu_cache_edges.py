@@ -60,3 +60,17 @@ def test_copy_between_views_of_one_pool(lib, how, order):
         t.copy_pages(ints(src), ints(dst), source=f)
         torch.cuda.synchronize()
         assert torch.equal(pool.k, want[0]) and torch.equal(pool.v, want[1]), turn
+
+
+def test_tensors_cannot_be_replaced(lib):
+    """The library keeps the addresses: an assignment that it would not notice is refused."""
+    cache = make(lib)
+    other = make(lib, layers=3, pages=41, P=8, heads_kv=3, d=64, slots=7, max_pages=9)
+    for name in ("k", "v", "table", "lengths", "refs", "layers", "pages", "heads_kv", "page_size", "head_dim",
+                 "slots", "max_pages"):
+        with pytest.raises(AttributeError, match="cannot be replaced"):
+            setattr(cache, name, getattr(other, name))
+    cache.name = "a user's own attribute"
+    cache.lengths[0] = 3        # contents are the caller's
+    cache.lengths += 1
+    assert cache.lengths.tolist()[0] == 4
