@@ -116,7 +116,21 @@ class CacheDesc(ctypes.Structure):
 
 
 # AttentionDesc's fields in order, with native alignment
-_DESC = struct.Struct("@iiiiiPPiiPfifQP24qqqiii0q")
+_DESC_CODES = "iiiii" "PP" "ii" "P" "f" "i" "f" "Q" "P" + "q" * 24 + "qq" "iii"
+_DESC = struct.Struct(f"@{_DESC_CODES}0q")
+
+
+def _pack(*values):
+    """An AttentionDesc's bytes.  What a field's type cannot hold becomes what the
+    library refuses there: an infinite scale or probability, a size of -1."""
+    try:
+        return _DESC.pack(*values)
+    except (OverflowError, struct.error):
+        bits = {"i": 31, "q": 63}
+        return _DESC.pack(*(ctypes.c_float(float(x)).value if c == "f"
+                            else -1 if c in bits and not -(1 << bits[c]) <= x < 1 << bits[c] else x
+                            for c, x in zip(_DESC_CODES, values)))
+
 
 _DP = ctypes.POINTER(AttentionDesc)
 _CP = ctypes.POINTER(CacheDesc)
@@ -433,7 +447,7 @@ def _desc(q, k, layout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, 
     sl, bm = _masks(seqlens_k, block_mask, device)
     get = {name: _strides(t, layout) for name, t in tensors.items()}.get
     # all fields at once (4 us less than one by one)
-    a = AttentionDesc.from_buffer_copy(_DESC.pack(
+    a = AttentionDesc.from_buffer_copy(_pack(
         *sizes, _ptr(sl) or 0, d ** -0.5 if scale is None else scale, bool(causal), dropout_p,
         int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(bm) or 0, *get("q", _UNUSED), *get("k", _UNUSED),
         *get("v", _UNUSED), *get("o", _UNUSED), *get("dout", _UNUSED), *get("dq", _UNUSED),

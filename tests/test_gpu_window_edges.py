@@ -53,3 +53,25 @@ def test_gradients_of_many_row_blocks(lib, H, Hkv, N, d, window, sinks):
         if h % G == G - 1:
             for n in ("dk", "dv"):  # (rounded once more, as plain64.padded says)
                 plain64.check(n, got[n][0, h // G], kv[n], kv[n + "_tol"] + plain64.BF16 * kv[n].abs())
+
+
+@pytest.mark.parametrize("kw", [dict(scale=1e300), dict(scale=-1e39), dict(dropout_p=1e39), dict(dropout_row0=2 ** 63),
+                                dict(dropout_key0=2 ** 64)])
+def test_values_beyond_fp32_are_refused_by_the_library(lib, kw):
+    q, k, v = (randn((1, 2, 64, 64), i) for i in range(3))
+    o, lse = lib.forward_general(q, k, v, causal=True, window=9)
+    with pytest.raises(lib.FaError) as e:
+        lib.forward_general(q, k, v, causal=True, window=9, **kw)
+    assert e.value.code == 1
+    with pytest.raises(lib.FaError) as e:
+        lib.backward_general(q, k, v, o, lse, q, causal=True, window=9, **kw)
+    assert e.value.code == 1
+
+
+def test_lengths_beyond_int_are_refused_by_the_library(lib):
+    q = randn((8, 2, 64), 1)
+    for n in (2 ** 31, 2 ** 32 + 8):
+        with pytest.raises(lib.FaError) as e:
+            lib.forward_general(q, q, q, layout="thd", cu_seqlens_q=[0, 8], cu_seqlens_k=[0, 8], max_seqlen_q=n,
+                                max_seqlen_k=8, causal=True)
+        assert e.value.code == 1
