@@ -94,6 +94,11 @@ class PagedCache:
                              "is expected")
         return st
 
+    def _layer(self, layer):
+        """-1, which the library refuses, for a layer that is none (a C int would
+        take 2^32 for 0)."""
+        return layer if 0 <= layer < self.layers else -1
+
     def _workspace(self, call, *n):
         key = (call, *n)
         size = self._sizes.get(key)
@@ -140,7 +145,7 @@ class PagedCache:
         if cu_seqlens is None and shape[0] != n:
             raise ValueError("write: one row per slot is expected without cu_seqlens")
         cu = None if cu_seqlens is None else self._ints("cu_seqlens", cu_seqlens, n + 1)
-        self._call(self._lib.fa_cache_write, layer, k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0],
+        self._call(self._lib.fa_cache_write, self._layer(layer), k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0],
                    sv[1], self._ints("slots", slots, n), self._ints("start", start, n), cu, n,
                    shape[0])
 
@@ -173,7 +178,7 @@ class PagedCache:
         if size is None:  # a function of the cache's sizes and these alone
             size = self._sizes[key] = self._lib.fa_cache_attend_workspace_size(self._ref, *key)
         ws = self.lengths.new_empty((size + 3) // 4) if size else None
-        self._call(self._lib.fa_cache_attend, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        self._call(self._lib.fa_cache_attend, self._layer(layer), q.data_ptr(), out.data_ptr(), lse.data_ptr(),
                    sq[0], sq[1], so[0], so[1],
                    None if slots is None else self._ints("slots", slots, B), B, H,
                    d ** -0.5 if scale is None else scale, window, sinks,

@@ -74,3 +74,17 @@ def test_tensors_cannot_be_replaced(lib):
     cache.lengths[0] = 3        # contents are the caller's
     cache.lengths += 1
     assert cache.lengths.tolist()[0] == 4
+
+
+@pytest.mark.parametrize("layer", [2, -1, 2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 32, 2 ** 70])
+def test_layers_out_of_range_are_refused(lib, layer):
+    cache = make(lib, layers=2)
+    model = CacheModel(cache)
+    start = cache.extend(ints([0]), ints([1]))
+    model.extend([0], [1])
+    k, q = randn((1, 2, 32), 1), randn((6, 4, 32), 2)
+    for call in (lambda: cache.write(layer, k, k, ints([0]), start), lambda: cache.attend(layer, q)):
+        with pytest.raises(lib.FaError) as e:
+            call()
+        assert e.value.code == 1
+    model.check(cache)
