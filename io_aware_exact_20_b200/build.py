@@ -9,10 +9,12 @@ Run ``python -m io_aware_exact_20_b200.build`` or call ``build()``.
 ``_build/<name>/`` (the binding loads it when ``FA_B200_LIBRARY`` names it):
 ``sanitize`` compiles the host code with AddressSanitizer and
 UndefinedBehaviorSanitizer (the process must preload their runtimes), and
-``bounds`` compiles the kernels with ``FA_DEBUG_BOUNDS``: every global-memory
-access they make outside TMA is checked against the extent of its buffer, and
+``bounds`` compiles the kernels with ``FA_DEBUG_BOUNDS``: the global-memory
+accesses that the attention kernels (forward, backward, decode) and the paged
+cache's make outside TMA are checked against the extent of their buffers, and
 one out of range is skipped and recorded in the device status word
-(FA_ERR_BOUNDS) instead of being made.
+(FA_ERR_BOUNDS) instead of being made.  (The merge, conversion, projection and
+test-support kernels walk flat arrays under one guard.)
 """
 
 from __future__ import annotations

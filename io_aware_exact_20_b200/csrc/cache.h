@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "fa.h"
+#include "kernels.h"
 
 namespace fa {
 
@@ -19,7 +20,27 @@ struct Cache {
   int32_t* refs;                         // [pages] or null
   int layers, pages, page_size, heads_kv, d;
   int slots, max_pages;
+#ifdef FA_DEBUG_BOUNDS
+  int* status;
+  long long ext_k, ext_v;                // elements from k, v to the pool's end
+#endif
 };
+
+// Element i of a list of n, and its store: what the kernels of the cache do to
+// memory goes through these (or FA_IN_BOUNDS itself), so that checking builds
+// skip and record an index beyond the list.
+template <typename T>
+__device__ __forceinline__ T get(const Cache& c, const T* list, long long i, long long n) {
+  return FA_IN_BOUNDS(c.status, i, 1, n) ? list[i] : T{};
+}
+template <typename T>
+__device__ __forceinline__ void put(const Cache& c, T* list, long long i, long long n, T x) {
+  if (FA_IN_BOUNDS(c.status, i, 1, n)) list[i] = x;
+}
+// Cells of the table, slots' rows end to end.
+__device__ __forceinline__ long long table_cells(const Cache& c) {
+  return static_cast<long long>(c.slots) * c.max_pages;
+}
 
 inline bool cache_aligned(const void* p, uintptr_t a) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
@@ -73,6 +94,15 @@ inline fa_status_t cache_resolve(const fa_cache_t* a, bool needs_refs, Cache* c)
   c->d = d;
   c->slots = a->slots;
   c->max_pages = a->max_pages;
+#ifdef FA_DEBUG_BOUNDS
+  c->status = device_status();
+  auto extent = [&](int64_t layer_stride, const fa_strides_t& st) -> long long {
+    return (a->layers - 1) * layer_stride + (a->pages - 1) * st.batch + (a->heads_kv - 1) * st.head +
+           (a->page_size - 1) * st.row + d;
+  };
+  c->ext_k = extent(a->k_layer, a->ks);
+  c->ext_v = extent(a->v_layer, a->vs);
+#endif
   return FA_OK;
 }
 

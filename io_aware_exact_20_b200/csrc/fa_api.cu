@@ -33,6 +33,12 @@ int* status_word() {
   }));
 }
 
+}  // namespace
+
+int* fa::device_status() { return status_word(); }
+
+namespace {
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool tensor_ok(const void* p) { return p != nullptr && aligned(p, 16); }
 

@@ -32,6 +32,7 @@ struct Moves {
   int32_t* src;
   int32_t* dst;
   int32_t* rows;
+  int cap;  // entries the lists can hold
 };
 
 // Inclusive prefix sum over the block's threads; *total gets the sum of all.
@@ -62,7 +63,7 @@ __device__ __forceinline__ int block_scan(int x, int* smem, int* total) {
 }
 
 __device__ __forceinline__ int slot_length(const Cache& c, int s) {
-  return min(max(c.lengths[s], 0), c.max_pages * c.page_size);
+  return min(max(get(c, c.lengths, s, c.slots), 0), c.max_pages * c.page_size);
 }
 
 // ---------------------------------------------------------------------------
@@ -88,12 +89,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
   // the first entry of each slot
   for (int i = tid; i < n; i += kPlanThreads) {
     const int s = slots[i];
-    if (s >= 0 && s < c.slots) w.mark[s] = INT_MAX;
+    if (s >= 0 && s < c.slots) put(c, w.mark, s, c.slots, INT_MAX);
   }
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
     const int s = slots[i];
-    if (s >= 0 && s < c.slots) atomicMin(&w.mark[s], i);
+    if (s >= 0 && s < c.slots && FA_IN_BOUNDS(c.status, s, 1, c.slots)) atomicMin(&w.mark[s], i);
   }
   __syncthreads();
   // pages each entry needs, and their running sum
@@ -104,15 +105,16 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
     if (i < n) {
       const int s = slots[i];
       const int more = tokens[i];
-      if (s >= 0 && s < c.slots && w.mark[s] == i && more >= 0) {
+      if (s >= 0 && s < c.slots && get(c, w.mark, s, c.slots) == i && more >= 0) {
         const int len = slot_length(c, s);
         const long long want = (static_cast<long long>(len) + more + P - 1) / P;
         if (want <= c.max_pages) {
           info = 2;
           const int have = (len + P - 1) / P;
           if (more > 0 && len % P != 0) {
-            const int page = c.table[static_cast<long long>(s) * c.max_pages + have - 1];
-            if (page >= 0 && page < c.pages && c.refs[page] > 1) info = 3;
+            const int page =
+                get(c, c.table, static_cast<long long>(s) * c.max_pages + have - 1, table_cells(c));
+            if (page >= 0 && page < c.pages && get(c, c.refs, page, c.pages) > 1) info = 3;
           }
           need = static_cast<int>(want) - have + (info & 1);
         }
@@ -122,8 +124,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
     const int upto = block_scan(need, scan, &total);  // at most 1024 * 2^20 + 1024
     if (i < n) {
       const long long u = need_all + upto;
-      w.upto[i] = static_cast<int>(u < INT_MAX ? u : INT_MAX);
-      w.info[i] = info | (need > 0 ? 4 : 0);
+      put(c, w.upto, i, w.moves.cap, static_cast<int>(u < INT_MAX ? u : INT_MAX));
+      put(c, w.info, i, w.moves.cap, info | (need > 0 ? 4 : 0));
     }
     need_all += total;
   }
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
     int mine = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      is_free[u] = p + u < c.pages && c.refs[p + u] <= 0;
+      is_free[u] = p + u < c.pages && get(c, c.refs, p + u, c.pages) <= 0;
       mine += is_free[u];
     }
     int total = 0;
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (is_free[u]) {
-        if (at < limit) w.free[at] = p + u;
+        if (at < limit) put(c, w.free, at, c.pages, p + u);
         ++at;
       }
     found += total;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
   // grant: a warp per entry, its lanes over the entry's new table cells
   const int lane = tid & 31;
   for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
-    const int info = w.info[i], upto = w.upto[i];
+    const int info = get(c, w.info, i, w.moves.cap), upto = get(c, w.upto, i, w.moves.cap);
     const bool granted = (info & 2) && (!(info & 4) || upto <= found);
     int copy_src = 0, copy_dst = 0, copy_rows = 0, first = -1;
     if (granted) {
@@ -162,29 +164,29 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Cache c, con
       const int have = (len + P - 1) / P, shared = info & 1;
       const int want = (len + tokens[i] + P - 1) / P;
       const int need = want - have + shared;
-      int32_t* row = c.table + static_cast<long long>(s) * c.max_pages;
+      const long long row = static_cast<long long>(s) * c.max_pages;  // of the table
       if (shared) {
-        copy_src = row[have - 1];
-        copy_dst = w.free[upto - need];
+        copy_src = get(c, c.table, row + have - 1, table_cells(c));
+        copy_dst = get(c, w.free, upto - need, c.pages);
         copy_rows = len % P;
       }
       __syncwarp();
       for (int j = lane; j < need; j += 32) {
-        const int page = w.free[upto - need + j];
-        row[have - shared + j] = page;
-        c.refs[page] = 1;
+        const int page = get(c, w.free, upto - need + j, c.pages);
+        put(c, c.table, row + have - shared + j, table_cells(c), page);
+        put(c, c.refs, page, c.pages, 1);
       }
       if (lane == 0) {
-        if (shared) atomicSub(&c.refs[copy_src], 1);
-        c.lengths[s] = len + tokens[i];
+        if (shared && FA_IN_BOUNDS(c.status, copy_src, 1, c.pages)) atomicSub(&c.refs[copy_src], 1);
+        put(c, c.lengths, s, c.slots, len + tokens[i]);
       }
       first = len;
     }
     if (lane == 0) {
       start[i] = first;
-      w.moves.src[i] = copy_src;
-      w.moves.dst[i] = copy_dst;
-      w.moves.rows[i] = copy_rows;
+      put(c, w.moves.src, i, w.moves.cap, copy_src);
+      put(c, w.moves.dst, i, w.moves.cap, copy_dst);
+      put(c, w.moves.rows, i, w.moves.cap, copy_rows);
     }
   }
   if (tid == 0) *w.moves.count = n;
@@ -207,21 +209,25 @@ __global__ void __launch_bounds__(256) move_kernel(const Cache from, const Cache
   for (long long it = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
        it < items; it += warps) {
     const int i = static_cast<int>(it / per_move);
-    const int rows = m.rows[i];
+    const int rows = get(from, m.rows, i, m.cap);
     if (rows == 0) continue;
+    const int page = get(from, m.src, i, m.cap), page_to = get(from, m.dst, i, m.cap);
     int r = static_cast<int>(it - i * per_move);
     const int h = r % from.heads_kv;
     r /= from.heads_kv;
     const int layer = r >> 1;
     const bool is_v = (r & 1) != 0;
-    const __nv_bfloat16* src =
-        static_cast<const __nv_bfloat16*>(is_v ? from.v : from.k) +
-        (is_v ? layer * from.v_layer + m.src[i] * from.v_page + h * from.v_head
-              : layer * from.k_layer + m.src[i] * from.k_page + h * from.k_head);
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) +
-                         (is_v ? layer * to.v_layer + m.dst[i] * to.v_page + h * to.v_head
-                               : layer * to.k_layer + m.dst[i] * to.k_page + h * to.k_head);
+    const long long src_at = is_v ? layer * from.v_layer + page * from.v_page + h * from.v_head
+                                  : layer * from.k_layer + page * from.k_page + h * from.k_head;
+    const long long dst_at = is_v ? layer * to.v_layer + page_to * to.v_page + h * to.v_head
+                                  : layer * to.k_layer + page_to * to.k_page + h * to.k_head;
     const long long src_row = is_v ? from.v_row : from.k_row, dst_row = is_v ? to.v_row : to.k_row;
+    // (a run of whole rows: its ends are the farthest elements)
+    if (!FA_IN_BOUNDS(from.status, src_at, (rows - 1) * src_row + from.d, is_v ? from.ext_v : from.ext_k) ||
+        !FA_IN_BOUNDS(to.status, dst_at, (rows - 1) * dst_row + to.d, is_v ? to.ext_v : to.ext_k))
+      continue;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? from.v : from.k) + src_at;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + dst_at;
     // eight loads in flight a lane, then their stores (697 MB read and written:
     // 116 us, 6.0 TB/s; with each load followed by its store 124)
     const int total = rows * chunks;
@@ -254,6 +260,9 @@ struct WriteParams {
   const int32_t* start;
   const int32_t* cu;
   int layer, n, total;
+#ifdef FA_DEBUG_BOUNDS
+  long long ext_k, ext_v;  // elements of the new rows
+#endif
 };
 
 __global__ void __launch_bounds__(256) write_kernel(const WriteParams p) {
@@ -269,26 +278,32 @@ __global__ void __launch_bounds__(256) write_kernel(const WriteParams p) {
     if (p.cu[0] > t || p.cu[p.n] <= t) return;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (p.cu[mid] <= t) lo = mid;
+      if (get(p.c, p.cu, mid, p.n + 1) <= t) lo = mid;
       else hi = mid;
     }
     i = lo;
-    within = t - p.cu[lo];
+    within = t - get(p.c, p.cu, lo, p.n + 1);
   }
-  const int first = p.start[i], s = p.slots[i];
+  const int first = get(p.c, p.start, i, p.n), s = get(p.c, p.slots, i, p.n);
   if (first < 0 || s < 0 || s >= p.c.slots) return;
   const long long pos = static_cast<long long>(first) + within;
   const long long cell = pos / p.c.page_size;
   if (cell >= p.c.max_pages) return;
-  const int page = p.c.table[static_cast<long long>(s) * p.c.max_pages + cell];
+  const int page = get(p.c, p.c.table, static_cast<long long>(s) * p.c.max_pages + cell, table_cells(p.c));
   if (page < 0 || page >= p.c.pages) return;
   const int row = static_cast<int>(pos - cell * p.c.page_size);
   const int chunks = p.c.d / 8, half = p.c.heads_kv * chunks;
   const __nv_bfloat16 *ks = p.k + t * p.k_row, *vs = p.v + t * p.v_row;
-  __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.c.k) + p.layer * p.c.k_layer +
-                      page * p.c.k_page + row * p.c.k_row;
-  __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.c.v) + p.layer * p.c.v_layer +
-                      page * p.c.v_page + row * p.c.v_row;
+  const long long k_at = p.layer * p.c.k_layer + page * p.c.k_page + row * p.c.k_row;
+  const long long v_at = p.layer * p.c.v_layer + page * p.c.v_page + row * p.c.v_row;
+  const int more = p.c.heads_kv - 1;  // (the last head's row is the farthest)
+  if (!FA_IN_BOUNDS(p.c.status, k_at, more * p.c.k_head + p.c.d, p.c.ext_k) ||
+      !FA_IN_BOUNDS(p.c.status, v_at, more * p.c.v_head + p.c.d, p.c.ext_v) ||
+      !FA_IN_BOUNDS(p.c.status, t * p.k_row, more * p.k_head + p.c.d, p.ext_k) ||
+      !FA_IN_BOUNDS(p.c.status, t * p.v_row, more * p.v_head + p.c.d, p.ext_v))
+    return;
+  __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(p.c.k) + k_at;
+  __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.c.v) + v_at;
   constexpr int kPieces = 4;  // loads in flight a lane, as in move_kernel
   for (int x0 = lane; x0 < 2 * half; x0 += 32 * kPieces) {
     uint4 v[kPieces];
@@ -317,6 +332,7 @@ __global__ void __launch_bounds__(256) write_kernel(const WriteParams p) {
 struct ForkWork {
   int32_t* rows;    // [n][max_pages]: the sources' table rows
   int32_t* lens;    // [n]: their lengths, -1 for entries that are skipped
+  int n;
 };
 
 __global__ void __launch_bounds__(256) fork_take_kernel(const Cache c, const int32_t* src,
@@ -328,17 +344,17 @@ __global__ void __launch_bounds__(256) fork_take_kernel(const Cache c, const int
   bool skip = s == d || s < 0 || s >= c.slots || d < 0 || d >= c.slots;
   for (int j = threadIdx.x; j < i; j += blockDim.x) skip = skip || dst[j] == d;
   if (__syncthreads_or(skip)) {
-    if (threadIdx.x == 0) w.lens[i] = -1;
+    if (threadIdx.x == 0) put(c, w.lens, i, w.n, -1);
     return;
   }
-  const int32_t* row = c.table + static_cast<long long>(s) * c.max_pages;
-  int32_t* out = w.rows + static_cast<long long>(i) * c.max_pages;
+  const long long row = static_cast<long long>(s) * c.max_pages;  // of the table
+  const long long out = static_cast<long long>(i) * c.max_pages;  // of the saved rows
   for (int j = threadIdx.x; j < c.max_pages; j += blockDim.x) {
-    const int page = row[j];
-    out[j] = page;
-    if (page >= 0 && page < c.pages) atomicAdd(&c.refs[page], 1);
+    const int page = get(c, c.table, row + j, table_cells(c));
+    put(c, w.rows, out + j, static_cast<long long>(w.n) * c.max_pages, page);
+    if (page >= 0 && page < c.pages && FA_IN_BOUNDS(c.status, page, 1, c.pages)) atomicAdd(&c.refs[page], 1);
   }
-  if (threadIdx.x == 0) w.lens[i] = slot_length(c, s);
+  if (threadIdx.x == 0) put(c, w.lens, i, w.n, slot_length(c, s));
 }
 
 __global__ void __launch_bounds__(256) fork_put_kernel(const Cache c, const int32_t* dst,
@@ -346,17 +362,17 @@ __global__ void __launch_bounds__(256) fork_put_kernel(const Cache c, const int3
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x;
-  const int len = w.lens[i];
+  const int len = get(c, w.lens, i, w.n);
   if (len < 0) return;
   const int d = dst[i];
-  int32_t* row = c.table + static_cast<long long>(d) * c.max_pages;
-  const int32_t* in = w.rows + static_cast<long long>(i) * c.max_pages;
+  const long long row = static_cast<long long>(d) * c.max_pages;  // of the table
+  const long long in = static_cast<long long>(i) * c.max_pages;   // of the saved rows
   for (int j = threadIdx.x; j < c.max_pages; j += blockDim.x) {
-    const int page = row[j];
-    if (page >= 0 && page < c.pages) atomicSub(&c.refs[page], 1);
-    row[j] = in[j];
+    const int page = get(c, c.table, row + j, table_cells(c));
+    if (page >= 0 && page < c.pages && FA_IN_BOUNDS(c.status, page, 1, c.pages)) atomicSub(&c.refs[page], 1);
+    put(c, c.table, row + j, table_cells(c), get(c, w.rows, in + j, static_cast<long long>(w.n) * c.max_pages));
   }
-  if (threadIdx.x == 0) c.lengths[d] = len;
+  if (threadIdx.x == 0) put(c, c.lengths, d, c.slots, len);
 }
 
 // The exchange lets a slot that is named twice go once.
@@ -365,12 +381,13 @@ __global__ void __launch_bounds__(256) free_kernel(const Cache c, const int32_t*
   griddep_launch_dependents();
   const int s = slots[blockIdx.x];
   if (s < 0 || s >= c.slots) return;
-  int32_t* row = c.table + static_cast<long long>(s) * c.max_pages;
+  const long long row = static_cast<long long>(s) * c.max_pages;  // of the table
   for (int j = threadIdx.x; j < c.max_pages; j += blockDim.x) {
-    const int page = atomicExch(&row[j], -1);
-    if (page >= 0 && page < c.pages) atomicSub(&c.refs[page], 1);
+    if (!FA_IN_BOUNDS(c.status, row + j, 1, table_cells(c))) continue;
+    const int page = atomicExch(&c.table[row + j], -1);
+    if (page >= 0 && page < c.pages && FA_IN_BOUNDS(c.status, page, 1, c.pages)) atomicSub(&c.refs[page], 1);
   }
-  if (threadIdx.x == 0) c.lengths[s] = 0;
+  if (threadIdx.x == 0) put(c, c.lengths, s, c.slots, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -390,7 +407,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Cache 
   const int tid = threadIdx.x;
   int mine = 0;
 #pragma unroll 8
-  for (int p = tid; p < c.pages; p += kPlanThreads) mine += c.refs[p] > 0;
+  for (int p = tid; p < c.pages; p += kPlanThreads) mine += get(c, c.refs, p, c.pages) > 0;
   int count = 0;
   block_scan(mine, scan, &count);
   // the k-th free page below `count` receives the k-th used one from it on;
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Cache 
     uint32_t used_bits = 0;
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      if (p + u < c.pages && c.refs[p + u] > 0) used_bits |= 1u << u;
+      if (p + u < c.pages && get(c, c.refs, p + u, c.pages) > 0) used_bits |= 1u << u;
     const uint32_t below = low_bits(min(kPer, count - p)), inside = low_bits(min(kPer, c.pages - p));
     const uint32_t hole_bits = below & inside & ~used_bits, mover_bits = ~below & used_bits;
     int total = 0;
@@ -411,20 +428,20 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Cache 
     int hole = holes + (at & 0xFFFF), mover = movers + (at >> 16);
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      if ((hole_bits >> u) & 1u) w.moves.dst[hole++] = p + u;
-      if ((mover_bits >> u) & 1u) w.moves.src[mover++] = p + u;
-      else if (p + u >= count && p + u < c.pages) w.now[p + u] = p + u;
+      if ((hole_bits >> u) & 1u) put(c, w.moves.dst, hole++, w.moves.cap, p + u);
+      if ((mover_bits >> u) & 1u) put(c, w.moves.src, mover++, w.moves.cap, p + u);
+      else if (p + u >= count && p + u < c.pages) put(c, w.now, p + u, c.pages, p + u);
     }
     holes += total & 0xFFFF;
     movers += total >> 16;
   }
   __syncthreads();
   for (int k = tid; k < movers; k += kPlanThreads) {
-    const int s = w.moves.src[k], d = w.moves.dst[k];
-    w.moves.rows[k] = c.page_size;
-    w.now[s] = d;
-    c.refs[d] = c.refs[s];
-    c.refs[s] = 0;
+    const int s = get(c, w.moves.src, k, w.moves.cap), d = get(c, w.moves.dst, k, w.moves.cap);
+    put(c, w.moves.rows, k, w.moves.cap, c.page_size);
+    put(c, w.now, s, c.pages, d);
+    put(c, c.refs, d, c.pages, get(c, c.refs, s, c.pages));
+    put(c, c.refs, s, c.pages, 0);
   }
   if (tid == 0) {
     *w.moves.count = movers;
@@ -437,11 +454,11 @@ __global__ void __launch_bounds__(256) renumber_kernel(const Cache c, const int3
   griddep_wait();
   griddep_launch_dependents();
   const int count = *used;
-  const long long cells = static_cast<long long>(c.slots) * c.max_pages;
+  const long long cells = table_cells(c);
   for (long long x = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; x < cells;
        x += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int page = c.table[x];
-    if (page >= count && page < c.pages) c.table[x] = now[page];
+    const int page = get(c, c.table, x, table_cells(c));
+    if (page >= count && page < c.pages) put(c, c.table, x, table_cells(c), get(c, now, page, c.pages));
   }
 }
 
@@ -458,25 +475,25 @@ struct Shared {
   long long by[kMost], from[kMost], to[kMost];
 };
 
-__global__ void __launch_bounds__(256) copy_plan_kernel(int pages_from, int pages_to, const Shared sh,
+__global__ void __launch_bounds__(256) copy_plan_kernel(const Cache from, const Cache to, const Shared sh,
                                                         const int32_t* src, const int32_t* dst,
-                                                        int n, int page_size, const Moves m) {
+                                                        int n, const Moves m) {
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x;
   const int s = src[i], d = dst[i];
-  bool skip = s < 0 || s >= pages_from || d < 0 || d >= pages_to;
+  bool skip = s < 0 || s >= from.pages || d < 0 || d >= to.pages;
   for (int j = threadIdx.x; j < n; j += blockDim.x) {
     skip = skip || (j < i && dst[j] == d);
     const int o = src[j];
-    if (o >= 0 && o < pages_from)
+    if (o >= 0 && o < from.pages)
       for (int k = 0; k < sh.n; ++k) skip = skip || sh.by[k] + o * sh.from[k] == d * sh.to[k];
   }
   skip = __syncthreads_or(skip);
   if (threadIdx.x == 0) {
-    m.src[i] = s;
-    m.dst[i] = d;
-    m.rows[i] = skip ? 0 : page_size;
+    put(to, m.src, i, m.cap, s);
+    put(to, m.dst, i, m.cap, d);
+    put(to, m.rows, i, m.cap, skip ? 0 : to.page_size);
     if (i == 0) *m.count = n;
   }
 }
@@ -503,6 +520,7 @@ Moves carve_moves(Carve* w, int64_t n) {
   m.src = w->take(n);
   m.dst = w->take(n);
   m.rows = w->take(n);
+  m.cap = static_cast<int>(n);
   return m;
 }
 
@@ -666,6 +684,10 @@ fa_status_t fa_cache_write(const fa_cache_t* cache, int layer, const void* k, co
   p.layer = layer;
   p.n = n;
   p.total = total;
+#ifdef FA_DEBUG_BOUNDS
+  p.ext_k = (total - 1) * k_row + (p.c.heads_kv - 1) * k_head + p.c.d;
+  p.ext_v = (total - 1) * v_row + (p.c.heads_kv - 1) * v_head + p.c.d;
+#endif
   return fa::done(fa::launch_overlapped(fa::write_kernel, dim3((static_cast<unsigned>(total) + 7) / 8),
                                         dim3(256), 0, static_cast<cudaStream_t>(stream), p));
 }
@@ -683,6 +705,7 @@ fa_status_t fa_cache_fork(const fa_cache_t* cache, const int32_t* src, const int
   fa::ForkWork w;
   w.lens = carve.take(n);
   w.rows = carve.take(static_cast<int64_t>(n) * c.max_pages);
+  w.n = n;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_overlapped(fa::fork_take_kernel, dim3(static_cast<unsigned>(n)),
                                         dim3(256), 0, s, c, src, dst, w);
@@ -750,7 +773,7 @@ fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from,
   if (!fa::shared_of(of, to, &shared)) return FA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_overlapped(fa::copy_plan_kernel, dim3(static_cast<unsigned>(n)), dim3(256),
-                                        0, s, of.pages, to.pages, shared, src, dst, n, to.page_size, m);
+                                        0, s, of, to, shared, src, dst, n, m);
   if (e == cudaSuccess)
     e = fa::launch_overlapped(fa::move_kernel, dim3(fa::move_blocks(to, n)), dim3(256), 0, s, of, to, m);
   return fa::done(e);

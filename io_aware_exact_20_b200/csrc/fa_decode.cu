@@ -69,7 +69,19 @@ struct AttendParams {
   int shares;
   float2* part_stat;      // [2 * shares][16]: maximum (log2 units), row sum
   float* part_acc;        // [2 * shares][16][D]
+#ifdef FA_DEBUG_BOUNDS
+  long long ext_k, ext_v;  // elements from the layer's k, v to the pool's end
+  long long ext_q, ext_o;
+#endif
 };
+
+// Rows of partial results and LSE entries of a call.
+__device__ __forceinline__ long long part_rows(const AttendParams& p) {
+  return p.part_stat != nullptr ? 32ll * p.shares : 0;
+}
+__device__ __forceinline__ long long lse_count(const AttendParams& p) {
+  return static_cast<long long>(p.batch) * p.heads;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   const int bytes = live ? 16 : 0;  // 0: sixteen zero bytes, nothing is read
@@ -77,6 +89,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Sixteen bytes of the pool, base its layer's first element.
+__device__ __forceinline__ void copy16(const AttendParams& p, uint32_t dst, const __nv_bfloat16* src,
+                                       const __nv_bfloat16* base, long long extent) {
+  if (FA_IN_BOUNDS(p.c.status, src - base, 8, extent)) cp_async16(dst, src, true);
+  else cp_async16(dst, base, false);
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -181,11 +199,14 @@ __device__ __forceinline__ Visible visible_of(int n, int window, int sinks) {
 __device__ __forceinline__ void write_row(const AttendParams& p, int b, int h, int col, float m, float sum,
                                           const float (&out)[8]) {
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) =
-      make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
-                 pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
+  const long long at = b * p.o_batch + h * p.o_head + col;
+  if (FA_IN_BOUNDS(p.c.status, at, 8, p.ext_o))
+    *reinterpret_cast<uint4*>(p.o + at) =
+        make_uint4(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv),
+                   pack_bf16(out[4] * inv, out[5] * inv), pack_bf16(out[6] * inv, out[7] * inv));
   if (col == 0)
-    p.lse[static_cast<long long>(b) * p.heads + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    put(p.c, p.lse, static_cast<long long>(b) * p.heads + h, lse_count(p),
+        sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2);
 }
 
 // out += f * eight consecutive sums
@@ -205,10 +226,10 @@ constexpr int kRowCost = 2;
 // its slot and length.
 template <int KT>
 __device__ __forceinline__ int tiles_of(const AttendParams& p, int b, int* slot, int* len) {
-  *slot = p.slots != nullptr ? p.slots[b] : b;
+  *slot = p.slots != nullptr ? get(p.c, p.slots, b, p.batch) : b;
   *len = 0;
   if (*slot >= 0 && *slot < p.c.slots)
-    *len = min(max(p.c.lengths[*slot], 0), p.c.max_pages * p.c.page_size);
+    *len = min(max(get(p.c, p.c.lengths, *slot, p.c.slots), 0), p.c.max_pages * p.c.page_size);
   return (visible_of(*len, p.window, p.sinks).count + KT - 1) / KT;
 }
 // What a row of that many tiles takes up in the shares.
@@ -335,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
         const int j = vis.key(u);
         const int cell = j / p.c.page_size;
         r.row = j - cell * p.c.page_size;
-        r.page = p.c.table[static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell];
+        r.page = get(p.c, p.c.table, static_cast<long long>(sq.slot[c.j]) * p.c.max_pages + cell,
+                     table_cells(p.c));
       }
       return r;
     };
@@ -366,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           const int row = s * RPI + row_l;
           const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
           if (!col_ok) break;
-          cp_async16(kdst + dst, k0 + s * RPI * p.c.k_row, true);
-          cp_async16(vdst + dst, v0 + s * RPI * p.c.v_row, true);
+          copy16(p, kdst + dst, k0 + s * RPI * p.c.k_row, p.k, FA_EXTENT(p.ext_k));
+          copy16(p, vdst + dst, v0 + s * RPI * p.c.v_row, p.v, FA_EXTENT(p.ext_v));
         }
         return;
       }
@@ -382,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           const int row = s * RPI + row_l;
           const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
           if (!col_ok) break;
-          cp_async16(kdst + dst, (row < cut ? k0 : k1) + s * RPI * p.c.k_row, true);
-          cp_async16(vdst + dst, (row < cut ? v0 : v1) + s * RPI * p.c.v_row, true);
+          copy16(p, kdst + dst, (row < cut ? k0 : k1) + s * RPI * p.c.k_row, p.k, FA_EXTENT(p.ext_k));
+          copy16(p, vdst + dst, (row < cut ? v0 : v1) + s * RPI * p.c.v_row, p.v, FA_EXTENT(p.ext_v));
         }
       } else {
 #pragma unroll
@@ -393,8 +415,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           const bool ok = (live >> row) & 1u;
           const uint32_t dst = row * C::ROW + ((c ^ (row & 7)) << 4);
           if (!col_ok) continue;
-          cp_async16(kdst + dst, ok ? kh + page * p.c.k_page + at_row * p.c.k_row : p.k, ok);
-          cp_async16(vdst + dst, ok ? vh + page * p.c.v_page + at_row * p.c.v_row : p.v, ok);
+          const __nv_bfloat16* ks = ok ? kh + page * p.c.k_page + at_row * p.c.k_row : p.k;
+          const __nv_bfloat16* vs = ok ? vh + page * p.c.v_page + at_row * p.c.v_row : p.v;
+          cp_async16(kdst + dst, ks, ok && FA_IN_BOUNDS(p.c.status, ks - p.k, 8, p.ext_k));
+          cp_async16(vdst + dst, vs, ok && FA_IN_BOUNDS(p.c.status, vs - p.v, 8, p.ext_v));
         }
       }
     };
@@ -455,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int col = 16 * kk + 8 * u + 2 * q4;
-              qb[nb][kk][u] = h < hn && col < p.c.d
+              qb[nb][kk][u] = h < hn && col < p.c.d &&
+                                      FA_IN_BOUNDS(p.c.status, q0 + h * p.q_head + col - p.q, 2, p.ext_q)
                                   ? *reinterpret_cast<const uint32_t*>(q0 + h * p.q_head + col)
                                   : 0u;
             }
@@ -585,10 +610,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
             const int h = 8 * nb + 2 * q4 + u;
             if (g == 0 && h < hn) {
               if (whole)
-                p.lse[static_cast<long long>(b) * p.heads + h0 + h] =
-                    l[nb][u] == 0.f ? -INFINITY : (m[nb][u] + log2f(l[nb][u])) * kLn2;
+                put(p.c, p.lse, static_cast<long long>(b) * p.heads + h0 + h, lse_count(p),
+                    l[nb][u] == 0.f ? -INFINITY : (m[nb][u] + log2f(l[nb][u])) * kLn2);
               else
-                p.part_stat[pr + h] = make_float2(m[nb][u], l[nb][u]);
+                put(p.c, p.part_stat, pr + h, part_rows(p), make_float2(m[nb][u], l[nb][u]));
             }
           }
           if (whole) {
@@ -601,14 +626,15 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
                 const uint32_t x =
                     transpose8x8(pack_bf16(o[nb][i][2 * r] * inv[0], o[nb][i][2 * r + 1] * inv[1]));
                 const int col = 16 * i + 8 * r;
-                if (8 * nb + g < hn && col < p.c.d) *reinterpret_cast<uint32_t*>(dst + col) = x;
+                if (8 * nb + g < hn && col < p.c.d && FA_IN_BOUNDS(p.c.status, dst + col - p.o, 2, p.ext_o))
+                  *reinterpret_cast<uint32_t*>(dst + col) = x;
               }
           } else {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int h = 8 * nb + 2 * q4 + u;
               float* dst = p.part_acc + (pr + h) * D + g;
-              if (h < hn)
+              if (h < hn && FA_IN_BOUNDS(p.c.status, pr + h, 1, part_rows(p)))
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                   dst[16 * i] = o[nb][i][u];
@@ -676,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
           continue;
         }
         const long long row = (2ll * blk0 + (begins ? 1 : 0)) * 16 + r;
+        if (!FA_IN_BOUNDS(p.c.status, row, 1, part_rows(p))) continue;
         float4* a = reinterpret_cast<float4*>(p.part_acc + row * D + col);
         a[0] = make_float4(out[0], out[1], out[2], out[3]);
         a[1] = make_float4(out[4], out[5], out[6], out[7]);
@@ -783,8 +810,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
         const int b = b0 + static_cast<int>(32 * warp + __ffs(none) - 1) * kSeqsPerThread + i;
         for (int x = lane; x < p.heads * (p.c.d / 8); x += 32) {
           const int h = x / (p.c.d / 8), col = 8 * (x % (p.c.d / 8));
-          *reinterpret_cast<uint4*>(p.o + b * p.o_batch + h * p.o_head + col) = make_uint4(0u, 0u, 0u, 0u);
-          if (col == 0) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
+          const long long at = b * p.o_batch + h * p.o_head + col;
+          if (FA_IN_BOUNDS(p.c.status, at, 8, p.ext_o))
+            *reinterpret_cast<uint4*>(p.o + at) = make_uint4(0u, 0u, 0u, 0u);
+          if (col == 0)
+            put(p.c, p.lse, static_cast<long long>(b) * p.heads + h, lse_count(p), -INFINITY);
         }
       }
     }
@@ -931,7 +961,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
   float m = -INFINITY, l = 0.f;
   if (hr < hn)
     for (uint32_t i = threadIdx.x / kJoinHeads; i < parts; i += kJoinThreads / kJoinHeads) {
-      const float2 st = p.part_stat[row_of(share_at(i), hr)];
+      const float2 st = get(p.c, p.part_stat, row_of(share_at(i), hr), part_rows(p));
       const float mm = fmaxf(m, st.x), ref = mm == -INFINITY ? 0.f : mm;
       l = l * fast_exp2(m - ref) + st.y * fast_exp2(st.x - ref);
       m = mm;
@@ -961,6 +991,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
 #pragma unroll 4
     for (uint32_t i = group; i < parts; i += GROUPS) {
       const long long row = row_of(share_at(i), r);
+      if (!FA_IN_BOUNDS(p.c.status, row, 1, part_rows(p))) continue;
       add_row8(out, fast_exp2(p.part_stat[row].x - ref), p.part_acc + row * D + col);
     }
   }
@@ -1145,6 +1176,12 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.sinks = sinks;
   p.part_stat = nullptr;
   p.part_acc = nullptr;
+#ifdef FA_DEBUG_BOUNDS
+  p.ext_k = p.c.ext_k - layer * p.c.k_layer;
+  p.ext_v = p.c.ext_v - layer * p.c.v_layer;
+  p.ext_q = (batch - 1) * q_batch + (heads - 1) * q_head + p.c.d;
+  p.ext_o = (batch - 1) * o_batch + (heads - 1) * o_head + p.c.d;
+#endif
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto launch = p.block_heads == 8 ? (p.c.d <= 64    ? fa::launch_attend<64, 1>
                                       : p.c.d <= 128 ? fa::launch_attend<128, 1>

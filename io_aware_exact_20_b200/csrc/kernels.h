@@ -76,6 +76,9 @@ __host__ __device__ inline void grid_unit(long long u, int bh_total, int tiles, 
 // Device status codes written to the per-device status word.
 enum : int { kStatusOk = 0, kStatusInternal = 3, kStatusTimeout = 4, kStatusBounds = 6 };
 
+// Device address of the current device's status word (null on failure).
+int* device_status();
+
 // Builds with FA_DEBUG_BOUNDS check every global-memory access the kernels
 // make outside TMA (tensor maps clip by themselves) against the extent of its
 // buffer: elements from the base pointer to one past the last element the call
@@ -93,8 +96,10 @@ __device__ __forceinline__ bool in_bounds(int* status, long long off, long long 
   return false;
 }
 #define FA_IN_BOUNDS(status, off, width, extent) ::fa::in_bounds((status), (off), (width), (extent))
+#define FA_EXTENT(x) (x)  // an extent handed to a function that checks
 #else
 #define FA_IN_BOUNDS(status, off, width, extent) true
+#define FA_EXTENT(x) 0ll
 #endif
 
 // Bits 0 .. n-1 of a word (none for n <= 0, all for n >= 32).
