@@ -28,9 +28,11 @@ class PagedCache:
     _FIXED = frozenset(("k", "v", "table", "lengths", "refs", "layers", "pages", "heads_kv", "page_size",
                         "head_dim", "slots", "max_pages", "device"))
 
+    _sizes = None  # (set last; reading __dict__ here would slow every attribute's load down)
+
     def __setattr__(self, name, value):
         # (the same tensor comes back from an in-place operator, `cache.lengths += 1`)
-        if name in self._FIXED and "_sizes" in self.__dict__ and value is not getattr(self, name):
+        if name in self._FIXED and self._sizes is not None and value is not getattr(self, name):
             raise AttributeError(f"PagedCache.{name} cannot be replaced: its address and sizes are the "
                                  "library's already; make another PagedCache")
         object.__setattr__(self, name, value)
@@ -94,16 +96,11 @@ class PagedCache:
                              "is expected")
         return st
 
-    def _layer(self, layer):
-        """-1, which the library refuses, for a layer that is none (a C int would
-        take 2^32 for 0)."""
-        return layer if 0 <= layer < self.layers else -1
-
-    def _workspace(self, call, *n):
-        key = (call, *n)
-        size = self._sizes.get(key)
+    def _workspace(self, call, n):
+        size = self._sizes.get((call, n))
         if size is None:  # a function of the cache's sizes and n alone
-            size = self._sizes[key] = getattr(self._lib, f"fa_cache_{call}_workspace_size")(self._ref, *n)
+            args = (self._ref,) if n is None else (self._ref, n)
+            size = self._sizes[call, n] = getattr(self._lib, f"fa_cache_{call}_workspace_size")(*args)
         return self.lengths.new_empty(size // 4), size
 
     def _call(self, fn, *args):
@@ -134,6 +131,8 @@ class PagedCache:
         start[i], start[i] + 1, ... of slots[i]: one row per entry, or with
         cu_seqlens (int32 [n + 1]) rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1."""
         n, bf16, index = slots.numel(), self._bf16, self._index
+        if not 0 <= layer < self.layers:
+            layer = -1  # refused by the library (a C int would take 2^32 for 0)
         shape = k.shape
         if (len(shape) != 3 or shape[1] != self.heads_kv or shape[2] != self.head_dim
                 or v.shape != shape):
@@ -145,7 +144,7 @@ class PagedCache:
         if cu_seqlens is None and shape[0] != n:
             raise ValueError("write: one row per slot is expected without cu_seqlens")
         cu = None if cu_seqlens is None else self._ints("cu_seqlens", cu_seqlens, n + 1)
-        self._call(self._lib.fa_cache_write, self._layer(layer), k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0],
+        self._call(self._lib.fa_cache_write, layer, k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0],
                    sv[1], self._ints("slots", slots, n), self._ints("start", start, n), cu, n,
                    shape[0])
 
@@ -155,6 +154,8 @@ class PagedCache:
         its slot (slots int32 [B]; None: slot b for query b), with a window and
         first tokens as in forward_general.  The newest token has to be in the
         cache.  LSE: fp32 [B, H]."""
+        if not 0 <= layer < self.layers:
+            layer = -1  # as in write
         shape = q.shape
         if len(shape) != 3 or shape[2] != self.head_dim:
             raise ValueError(f"q: [B, H, {self.head_dim}] is expected")
@@ -178,7 +179,7 @@ class PagedCache:
         if size is None:  # a function of the cache's sizes and these alone
             size = self._sizes[key] = self._lib.fa_cache_attend_workspace_size(self._ref, *key)
         ws = self.lengths.new_empty((size + 3) // 4) if size else None
-        self._call(self._lib.fa_cache_attend, self._layer(layer), q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        self._call(self._lib.fa_cache_attend, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
                    sq[0], sq[1], so[0], so[1],
                    None if slots is None else self._ints("slots", slots, B), B, H,
                    d ** -0.5 if scale is None else scale, window, sinks,
@@ -204,7 +205,7 @@ class PagedCache:
         """Moves the pages in use into the lowest numbers; returns how many there
         are (int32 [1], on the device)."""
         used = self.lengths.new_empty(1)
-        ws, size = self._workspace("compact")
+        ws, size = self._workspace("compact", None)
         self._call(self._lib.fa_cache_compact, used.data_ptr(), ws.data_ptr(), size)
         return used
 
