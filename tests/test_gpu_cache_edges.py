@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from cache_model import CacheModel
-from test_gpu_cache import check_attend, ints, make, randn
+from test_gpu_cache import check_attend, filled, ints, make, randn, widened
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,66 @@ def test_layers_out_of_range_are_refused(lib, layer):
             call()
         assert e.value.code == 1
     model.check(cache)
+
+
+def test_calls_follow_the_current_stream(lib):
+    """Nothing between the first copy and the last call looks at the device: a call
+    sent to another stream would find the poisoned arguments."""
+    d, H, Hkv = 64, 4, 2
+    cache = make(lib, pages=30, P=4, d=d, heads_kv=Hkv, layers=1, slots=3, max_pages=12)
+    model = CacheModel(cache)
+    good = [ints([0, 1, 2]), ints([13, 20, 1]), ints([0, 13, 33, 34]), randn((34, Hkv, d), 1), randn((34, Hkv, d), 2),
+            randn((3, H, d), 3)]
+    slots, tokens, cu, k, v, q = [torch.full_like(t, -1 if t.dtype == torch.int32 else float("nan")) for t in good]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        for to, t in zip((slots, tokens, cu, k, v, q), good):
+            to.copy_(t)
+        start = cache.extend(slots, tokens)
+        cache.write(0, k, v, slots, start, cu_seqlens=cu)
+        o, lse = cache.attend(0, q, slots)
+    torch.cuda.synchronize()
+    assert start.tolist() == model.extend([0, 1, 2], [13, 20, 1])
+    model.write(0, good[3], good[4], [0, 1, 2], [0, 0, 0], [0, 13, 33, 34])
+    model.check(cache)
+    check_attend(cache, 0, good[5], [0, 1, 2], o, lse, d ** -0.5)
+
+
+@pytest.mark.parametrize("lens,columns", [([500, 3, 70], None), ([9000, 500, 20000, 1], 40000)])
+def test_two_calls_at_once(lib, lens, columns):
+    """Calls that overlap on two streams, each with its own workspace: the bits of
+    the calls one after the other."""
+    caches = [filled(lib, lens, 16, 2, 128, seed=s) for s in (41, 42)]
+    if columns:
+        caches = [widened(lib, c, columns) for c in caches]
+    qs = [randn((len(lens), 8, 128), s) for s in (43, 44)]
+    want = [c.attend(0, q) for c, q in zip(caches, qs)]
+    streams = [torch.cuda.Stream() for _ in caches]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for turn in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(caches[i].attend(0, qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("columns", [None, 40000])
+def test_mostly_idle_slots(lib, columns):
+    """A batch of a fixed size with most of its slots unused or empty."""
+    r = random.Random(6)
+    lens = [0] * 512
+    for s in r.sample(range(512), 12):
+        lens[s] = r.randint(1, 700)
+    cache = filled(lib, lens, 16, 2, 128, seed=45)
+    if columns:
+        cache = widened(lib, cache, columns)
+    slots = [s if lens[s] or r.random() < 0.5 else -1 for s in range(512)]
+    q = randn((512, 4, 128), 46)
+    o, lse = cache.attend(0, q, ints(slots))
+    check_attend(cache, 0, q, slots, o, lse, 128 ** -0.5)

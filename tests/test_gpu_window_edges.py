@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import plain64
-from test_gpu_window import randn, run
+from test_gpu_window import compare, randn, run
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,99 @@ def test_lengths_beyond_int_are_refused_by_the_library(lib):
             lib.forward_general(q, q, q, layout="thd", cu_seqlens_q=[0, 8], cu_seqlens_k=[0, 8], max_seqlen_q=n,
                                 max_seqlen_k=8, causal=True)
         assert e.value.code == 1
+
+
+@pytest.mark.parametrize("layout,B,H,Hkv,d,lens,mask", [
+    ("bshd", 2, 2, 1, 64, [2300, 700], False), ("bhsd", 1, 2, 2, 128, [90], False), ("bshd", 1, 2, 1, 128, None, True),
+    ("bhsd", 2, 4, 2, 64, [0, 2299], True), ("bhsd", 1, 2, 1, 256, [1500], True)])
+def test_first_keys_in_pieces_under_other_masks(lib, layout, B, H, Hkv, d, lens, mask):
+    """The first keys' walks cut into pieces, with key lengths (some before the
+    window, some that hide first keys) and a block mask (whole pieces of it empty)."""
+    N, window, sinks = 2300, 150, 140
+    q, do = randn((B, H, N, d), 21), randn((B, H, N, d), 22)
+    k, v = randn((B, Hkv, N, d), 23), randn((B, Hkv, N, d), 24)
+    bm = None
+    if mask:
+        nb = (N + 127) // 128
+        bm = torch.ones((nb, nb), dtype=torch.uint8, device="cuda")
+        bm[7:, 1] = 0       # the second tile of first keys is hidden from there on
+        bm[10:15, 0] = 0
+        bm[4, 3:5] = 0
+    ref = plain64.padded(q, k, v, d ** -0.5, lambda b: plain64.visible(
+        N, N, q.device, window=window, sinks=sinks, kv_len=None if lens is None else lens[b], block_mask=bm), do)
+    turn = (lambda t: t) if layout == "bhsd" else (lambda t: t.transpose(1, 2).contiguous())
+    got = run(lib, *(turn(t) for t in (q, k, v, do)), layout=layout, causal=True, window=window, sinks=sinks,
+              seqlens_k=lens, block_mask=bm)
+    if layout == "bshd":
+        for n in ("o", "dq", "dk", "dv"):
+            got[n] = got[n].transpose(1, 2)
+    compare(got, ref)
+
+
+@pytest.mark.parametrize("d,H,Hkv", [(64, 2, 2), (128, 4, 1)])
+def test_first_keys_in_pieces_of_sequences_without_queries(lib, d, H, Hkv):
+    """A packed batch in which sequences without queries, or shorter than a piece,
+    stand between long ones: their keys' gradients are zero, and so is nobody else's row touched."""
+    window, sinks = 100, 130
+    lq, lk = [0, 2400, 0, 5, 2200, 0], [300, 2400, 1, 2000, 2300, 129]
+    cq, ck = [0] + torch.tensor(lq).cumsum(0).tolist(), [0] + torch.tensor(lk).cumsum(0).tolist()
+    q, do = randn((cq[-1], H, d), 31), randn((cq[-1], H, d), 32)
+    k, v = randn((ck[-1], Hkv, d), 33), randn((ck[-1], Hkv, d), 34)
+    r = run(lib, q, k, v, do, layout="thd", cu_seqlens_q=cq, cu_seqlens_k=ck, max_seqlen_q=max(lq), max_seqlen_k=max(lk),
+            causal=True, window=window, sinks=sinks)
+    for b, (n, m) in enumerate(zip(lq, lk)):
+        rq, rk = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b + 1])
+        if n == 0:
+            assert (r["dk"][rk] == 0).all() and (r["dv"][rk] == 0).all()
+            continue
+        part = lambda t, s: t[s].transpose(0, 1)[None]  # noqa: E731
+        ref = plain64.padded(part(q, rq), part(k, rk), part(v, rk), d ** -0.5,
+                             lambda _: plain64.visible(n, m, q.device, window=window, sinks=sinks), part(do, rq))
+        compare(dict(o=part(r["o"], rq), dq=part(r["dq"], rq), dk=part(r["dk"], rk), dv=part(r["dv"], rk),
+                     lse=r["lse"][:, rq][None]), ref)
+
+
+def test_replay_leaves_eager_results_alone(lib):
+    """Results of an uncaptured run are the caller's: a graph of the same tensors
+    replayed twice, on other contents, does not touch them."""
+    N, d, kw = 600, 128, dict(causal=True, window=100, sinks=4)
+    q, k, v, do = (randn((1, 4, N, d), 50 + i) for i in range(4))
+    eager = run(lib, q, k, v, do, **kw)
+    keep = {n: t.clone() for n, t in eager.items()}
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        o, lse = lib.forward_general(q, k, v, **kw)
+        lib.backward_general(q, k, v, o, lse, do, **kw)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, keep["o"]) and torch.equal(lse, keep["lse"])
+    q.copy_(randn(q.shape, 60))
+    g.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(o, keep["o"])
+    for n, t in eager.items():
+        assert torch.equal(t, keep[n]), n
+
+
+def test_two_backwards_at_once(lib):
+    """Overlapping calls on two streams, each with its own workspace."""
+    d, kw = 64, dict(causal=True, window=70, sinks=5)
+    sets = [[randn((1, 4, 2300, d), 10 * i + j) for j in range(4)] for i in (7, 8)]
+    want = [run(lib, *s, **kw) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(4):
+        for s, t in zip(streams, sets):
+            with torch.cuda.stream(s):
+                o, lse = lib.forward_general(*t[:3], **kw)
+                got.append((o, lse) + tuple(lib.backward_general(*t[:3], o, lse, t[3], **kw)))
+    torch.cuda.synchronize()
+    assert lib.last_device_status() == 0
+    for i, (o, lse, dq, dk, dv) in enumerate(got):
+        w = want[i % 2]
+        assert all(torch.equal(a, w[n]) for a, n in ((o, "o"), (lse, "lse"), (dk, "dk"), (dv, "dv")))
+        # dQ is summed by atomics, in fp32: the order shows in a bf16 step at most (2^-7 of the value)
+        assert ((dq.float() - w["dq"].float()).abs() <= 2.0 ** -7 * w["dq"].float().abs() + 1e-6).all()
