@@ -1013,6 +1013,7 @@ struct Plan {
   int cluster;      // > 0: a cluster of that many blocks per row
   long long grid;
   bool cut;
+  int join_heads;   // of a joining block: one where few rows are joined, from many parts each
   size_t off_acc, bytes;
 };
 
@@ -1052,6 +1053,7 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
            : p.tiles < 148ll * per_sm ? p.tiles
                                       : 148ll * per_sm;
   p.cut = p.cluster == 0 && tiles > 1;
+  p.join_heads = rows * HB <= 4 * 148 ? 1 : 4;
   const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
   p.off_acc = parts * sizeof(float2);
   p.bytes = p.cut ? p.off_acc + parts * D * sizeof(float) : 0;
@@ -1112,9 +1114,7 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
   cudaError_t r = launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), dim3(kThreads), C::SMEM,
                                     stream, a);
   if (r == cudaSuccess && plan.cut)
-    r = p.batch * p.c.heads_kv * p.head_blocks * p.block_heads <= 4 * 148
-            ? launch_join<D, C::KT, 1>(a, stream)
-            : launch_join<D, C::KT, 4>(a, stream);
+    r = plan.join_heads == 1 ? launch_join<D, C::KT, 1>(a, stream) : launch_join<D, C::KT, 4>(a, stream);
   return r;
 }
 

@@ -61,3 +61,14 @@ def test_tensors_of_a_cache_cannot_be_replaced(lib):
     cache.lengths += 1
     cache.label = "a user's own attribute"
     assert cache.lengths.tolist() == [1, 1, 1] and cache.pages == 4
+
+
+def test_plans_of_the_largest_batches(lib):
+    """Counts of rows past 2^31 / 8 (undefined behaviour in 32 bits, which the sanitizer build reports)."""
+    so = lib.library()
+    c = desc(lib, heads_kv=1, head_dim=32, max_pages=4, page_size=16, slots=1)
+    for batch in (1 << 20, 1 << 28, (1 << 31) - 1):
+        assert so.fa_cache_attend_workspace_size(ctypes.byref(c), batch, 1, 0, 0) > 0
+    # more rows than the 32-bit counts of tiles hold are refused before any launch
+    a = [0, A16, A16, A16, 32, 32, 32, 32, None, (1 << 31) - 1, 1, 0.125, 0, 0, A16, 1 << 40, None]
+    assert so.fa_cache_attend(ctypes.byref(c), *a) == 2
