@@ -69,6 +69,9 @@ struct AttendParams {
   int shares;
   float2* part_stat;      // [2 * shares][16]: maximum (log2 units), row sum
   float* part_acc;        // [2 * shares][16][D]
+  // [batch + 1]: spans of the sequences before each, and of all, for batches that
+  // are longer than a joining block should add up by itself; else null
+  uint32_t* spans;
 #ifdef FA_DEBUG_BOUNDS
   long long ext_k, ext_v;  // elements from the layer's k, v to the pool's end
   long long ext_q, ext_o;
@@ -828,10 +831,16 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
   uint32_t chunk_lo = 0;  // tile at which the chunk of sequences begins
   int b_from = 0;
   if (p.batch > kSeqs) {
-    uint32_t from_lo = W;
+    uint32_t from_lo = W, before = 0;  // spans before the chunk
+    const bool tells = p.spans != nullptr && blockIdx.x == 0;
+    if (tells && threadIdx.x == 0) put(p.c, p.spans, p.batch, p.batch + 1ll, sum);
     for (int b0 = 0; b0 < p.batch; b0 += kSeqs) {
       part = load_seqs(b0);
       write_empty(b0);
+      if (tells)
+        for (int j = threadIdx.x; j < kSeqs && b0 + j < p.batch; j += kThreads)
+          put(p.c, p.spans, b0 + j, p.batch + 1ll, before + sq.upto[j] - span_of(sq.tiles[j]));
+      before += part;
       const uint32_t next_lo = chunk_lo + part * rows_per_seq;
       if (blk_from >= chunk_lo && blk_from < next_lo) {
         const int j = seq_at(blk_from, chunk_lo, b0);
@@ -889,6 +898,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
 // the lengths alone, so all of that happens before the wait for the attention
 // kernel (which starts its dependents only once the kernels before it are done):
 // small enough to be resident beside it, a block goes on at once when it ends.
+// Above kSeqs sequences the attention kernel's first block has written their
+// running sums instead: a block that adds up the whole batch, once per row, is
+// quadratic (8 K / V heads of 64: 1000 sequences of 100 keys 82 us, 77 with the
+// sums; 16000 of 60 keys 2515 and 762; 60000 of 40 keys 28700 and 2720).
 constexpr int kJoinThreads = 256;
 
 template <int D, int KT, int kJoinHeads>
@@ -901,33 +914,37 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
   const int b = blockIdx.x / rows_per_seq, rs = blockIdx.x - b * rows_per_seq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint2 sum = make_uint2(0u, 0u);  // spans of all sequences, and of those before b
-#pragma unroll 4
-  for (int i = threadIdx.x; i < p.batch; i += kJoinThreads) {
-    int slot, len;
-    const uint32_t span = span_of(tiles_of<KT>(p, i, &slot, &len));
-    sum.x += span;
-    sum.y += i < b ? span : 0u;
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
-    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
-  }
-  if (lane == 0) seqs[warp] = sum;
   int slot, len;
   const int tiles = tiles_of<KT>(p, b, &slot, &len);
-  __syncthreads();
-  sum = make_uint2(0u, 0u);
+  if (p.spans == nullptr) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.batch; i += kJoinThreads) {
+      int s, n;
+      const uint32_t span = span_of(tiles_of<KT>(p, i, &s, &n));
+      sum.x += span;
+      sum.y += i < b ? span : 0u;
+    }
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    sum.x += seqs[w].x;
-    sum.y += seqs[w].y;
+    for (int o = 1; o < 32; o <<= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+    }
+    if (lane == 0) seqs[warp] = sum;
+    __syncthreads();
+    sum = make_uint2(0u, 0u);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      sum.x += seqs[w].x;
+      sum.y += seqs[w].y;
+    }
   }
   griddep_launch_dependents();
   // one block waits whatever its row: this grid must not be done before the
   // attention kernel is, or a kernel behind it could start beside that one
-  if (blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
+  if (p.spans != nullptr || (blockIdx.x == 0 && blockIdx.y == 0)) griddep_wait();
   if (tiles == 0) return;
+  if (p.spans != nullptr)
+    sum = make_uint2(get(p.c, p.spans, p.batch, p.batch + 1ll), get(p.c, p.spans, b, p.batch + 1ll));
   const uint32_t W = sum.x * rows_per_seq;
   const Shares sh(W, min(max(W, 1u), static_cast<uint32_t>(p.shares)));
   const uint32_t lo = sum.y * rows_per_seq + rs * span_of(tiles), hi = lo + tiles;
@@ -1014,7 +1031,7 @@ struct Plan {
   long long grid;
   bool cut;
   int join_heads;   // of a joining block: one where few rows are joined, from many parts each
-  size_t off_acc, bytes;
+  size_t off_acc, off_spans, bytes;
 };
 
 template <int NB>
@@ -1056,7 +1073,10 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   p.join_heads = rows * HB <= 4 * 148 ? 1 : 4;
   const size_t parts = static_cast<size_t>(p.grid) * kWarps * 2 * 16;
   p.off_acc = parts * sizeof(float2);
-  p.bytes = p.cut ? p.off_acc + parts * D * sizeof(float) : 0;
+  p.off_spans = p.off_acc + parts * D * sizeof(float);
+  p.bytes = !p.cut          ? 0
+            : batch > kSeqs ? p.off_spans + (static_cast<size_t>(batch) + 1) * sizeof(uint32_t)
+                            : p.off_spans;
   return p;
 }
 
@@ -1110,6 +1130,7 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
     char* ws = static_cast<char*>(workspace);
     a.part_stat = reinterpret_cast<float2*>(ws);
     a.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
+    if (p.batch > kSeqs) a.spans = reinterpret_cast<uint32_t*>(ws + plan.off_spans);
   }
   cudaError_t r = launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), dim3(kThreads), C::SMEM,
                                     stream, a);
@@ -1176,6 +1197,7 @@ fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, v
   p.sinks = sinks;
   p.part_stat = nullptr;
   p.part_acc = nullptr;
+  p.spans = nullptr;
 #ifdef FA_DEBUG_BOUNDS
   p.ext_k = p.c.ext_k - layer * p.c.k_layer;
   p.ext_v = p.c.ext_v - layer * p.c.v_layer;

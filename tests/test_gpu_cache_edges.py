@@ -151,3 +151,23 @@ def test_mostly_idle_slots(lib, columns):
     q = randn((512, 4, 128), 46)
     o, lse = cache.attend(0, q, ints(slots))
     check_attend(cache, 0, q, slots, o, lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("B,Hkv,G,window,sinks", [(513, 2, 4, 0, 0), (5000, 2, 1, 0, 0), (2100, 1, 17, 40, 5)])
+def test_rows_cut_in_batches_of_many_chunks(lib, B, Hkv, G, window, sinks):
+    """More sequences than a joining block adds up by itself: long ones, whose rows
+    are cut, at the ends of the batch and of the blocks' chunks of sequences."""
+    r = random.Random(B)
+    lens = [r.choice([0, 1, 16, 17, r.randrange(90)]) for _ in range(B)]
+    long = [0, 511, 512, B // 2, B - 1]
+    for b in long:
+        lens[b] = r.randint(3000, 6000)
+    cache = filled(lib, lens, 16, Hkv, 64, seed=47)
+    q = randn((B, Hkv * G, 64), 48)
+    o, lse = cache.attend(0, q, window=window, sinks=sinks)
+    some = sorted(set(long + [r.randrange(B) for _ in range(20)]))
+    check_attend(cache, 0, q[some], some, o[some], lse[some], 64 ** -0.5, window, sinks)
+    empty = [b for b in range(B) if lens[b] == 0]
+    assert (o[empty] == 0).all() and (lse[empty] == float("-inf")).all()
+    again = cache.attend(0, q, window=window, sinks=sinks)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
