@@ -382,7 +382,7 @@ fa_status_t fa_cache_write(const fa_cache_t* cache, int layer, const void* k, co
 /* Slot dst[i] lets its pages go and takes src[i]'s pages and length, i < n; all
  * sources are read before any destination is replaced, so beams can be
  * permuted in one call.  An entry with src[i] == dst[i], a slot out of range
- * or the destination of an earlier entry is skipped. */
+ * or the destination of an earlier entry is skipped.  n <= 2^20. */
 fa_status_t fa_cache_fork(const fa_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
                           void* workspace, size_t workspace_bytes, void* stream);
 
@@ -402,7 +402,7 @@ fa_status_t fa_cache_compact(const fa_cache_t* cache, int32_t* used, void* works
  * destination is any pair's source: within one cache, or where the two are views
  * of one pool with the same layer, head and row strides (their pages or layers
  * apart, or every n-th page), in any layer.  Caches that share memory in another
- * way, parts of pages, are not told apart. */
+ * way, parts of pages, are not told apart.  n <= 2^20. */
 fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from, const int32_t* src,
                                 const int32_t* dst, int n, void* workspace,
                                 size_t workspace_bytes, void* stream);

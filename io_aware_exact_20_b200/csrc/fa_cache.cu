@@ -24,6 +24,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;  // one block: its scans order entries and pages
 constexpr int kSms = 148;
+// Entries of a fork or a page copy: each looks at all others for its destination,
+// 0.4 s (fork) and 1 s (copy) at this many, and four times that at twice.
+constexpr int kMaxPairs = 1 << 20;
 
 // Moves of a call, in the workspace: page src[i] -> dst[i], its first rows[i]
 // rows of every head and layer (0: nothing), i < *count.
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(256) renumber_kernel(const Cache c, const int3
 
 // Where the two caches of a copy share memory, page for page: page s of the
 // source lies (in some layer) where page d of the destination does iff
-// by + s * from == d * to, in elements.
+// by + s * from == d * to.
 struct Shared {
   static constexpr int kMost = 16;
   int n;
@@ -483,11 +486,14 @@ __global__ void __launch_bounds__(256) copy_plan_kernel(const Cache from, const 
   const int i = blockIdx.x;
   const int s = src[i], d = dst[i];
   bool skip = s < 0 || s >= from.pages || d < 0 || d >= to.pages;
-  for (int j = threadIdx.x; j < n; j += blockDim.x) {
-    skip = skip || (j < i && dst[j] == d);
-    const int o = src[j];
-    if (o >= 0 && o < from.pages)
-      for (int k = 0; k < sh.n; ++k) skip = skip || sh.by[k] + o * sh.from[k] == d * sh.to[k];
+  for (int j = threadIdx.x; j < i; j += blockDim.x) skip = skip || dst[j] == d;
+  for (int k = 0; k < sh.n; ++k) {
+    // the source's page that lies where page d does (each = 0: it has one page)
+    const long long at = d * sh.to[k] - sh.by[k], each = sh.from[k];
+    const long long o = each > 0 ? at / each : 0;
+    if (o * each != at || o < 0 || o >= from.pages) continue;
+    const int page = static_cast<int>(o);
+    for (int j = threadIdx.x; j < n; j += blockDim.x) skip = skip || src[j] == page;
   }
   skip = __syncthreads_or(skip);
   if (threadIdx.x == 0) {
@@ -571,10 +577,16 @@ bool shared_of(const Cache& of, const Cache& to, Shared* sh) {
       for (long long l = l0; l <= l1; ++l) {
         const long long by = apart + l * a.layer;
         if (by < low || by > high || (step > 0 ? by % step : by) != 0) continue;
+        // in steps (pages, where both have the same): K's and V's are mostly one
+        const long long unit = step > 0 ? step : 1;
+        bool known = false;
+        for (int i = 0; i < sh->n; ++i)
+          known = known || (sh->by[i] == by / unit && sh->from[i] == pf / unit && sh->to[i] == pt / unit);
+        if (known) continue;
         if (sh->n == Shared::kMost) return false;
-        sh->by[sh->n] = by;
-        sh->from[sh->n] = pf;
-        sh->to[sh->n++] = pt;
+        sh->by[sh->n] = by / unit;
+        sh->from[sh->n] = pf / unit;
+        sh->to[sh->n++] = pt / unit;
       }
     }
   return true;
@@ -699,6 +711,7 @@ fa_status_t fa_cache_fork(const fa_cache_t* cache, const int32_t* src, const int
   if (st != FA_OK) return st;
   if (n < 0) return FA_ERR_INVALID_ARG;
   if (n == 0) return FA_OK;
+  if (n > fa::kMaxPairs) return FA_ERR_UNSUPPORTED;
   if (!fa::ints_ok(src) || !fa::ints_ok(dst)) return FA_ERR_INVALID_ARG;
   if (!fa::workspace_ok(fa::fork_ints(c, n), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};
@@ -765,6 +778,7 @@ fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from,
       of.d != to.d)
     return FA_ERR_INVALID_ARG;
   if (n == 0) return FA_OK;
+  if (n > fa::kMaxPairs) return FA_ERR_UNSUPPORTED;
   if (!fa::ints_ok(src) || !fa::ints_ok(dst)) return FA_ERR_INVALID_ARG;
   if (!fa::workspace_ok(fa::moves_ints(n), workspace, workspace_bytes)) return FA_ERR_WORKSPACE;
   fa::Carve carve{static_cast<int32_t*>(workspace)};

@@ -72,3 +72,11 @@ def test_plans_of_the_largest_batches(lib):
     # more rows than the 32-bit counts of tiles hold are refused before any launch
     a = [0, A16, A16, A16, 32, 32, 32, 32, None, (1 << 31) - 1, 1, 0.125, 0, 0, A16, 1 << 40, None]
     assert so.fa_cache_attend(ctypes.byref(c), *a) == 2
+
+
+def test_lists_that_would_take_minutes_are_refused(lib):
+    """A fork and a page copy look at every pair of entries: at most 2^20 entries."""
+    c = desc(lib)
+    for n in ((1 << 20) + 1, (1 << 31) - 1):
+        for name in ("fork", "copy"):
+            assert calls(lib, c, n=n, nbytes=1 << 50)[name]() == 2, (name, n)
