@@ -17,6 +17,14 @@
 //             partial products are added into fp32 accumulators;
 //   bwd_post  dQ = bf16(scale * accumulator).
 //
+// Roundings below fp32, besides the outputs': P and dS are bf16 as operands of
+// the products with dO, Q and K (an instruction takes one type for both, and
+// fp16's range is too small for dS), P waits as fp16 for the dS phase (P <= 1;
+// 32 registers instead of 64, of a budget of 128), and D is computed from the
+// bf16 O that the forward stored.  Against 64 bits dQ and dK are 1.5 times as far
+// off as fp32 throughout with bf16 outputs would be, more where a row sees
+// two or three keys and its terms cancel.
+//
 // bwd_main roles (512 threads):
 //   warp 0        TMA producer: K, V once; per query tile Q, dO and the
 //                 128-row slices of LSE*log2e and D into a ring

@@ -261,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
     attend_kernel(const AttendParams p) {
   using C = DecodeCfg<D, NB>;
   constexpr int KT = C::KT, STAGES = C::STAGES;
+  // in this order: join_kernel, released below, reads lengths and slots before its
+  // own wait, so all that wrote them has to be done by then
   griddep_wait();
   griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
@@ -538,8 +540,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, NB>::MIN_BLOCKS)
       }
       // Online softmax over the tile's keys, per head of this lane's pair; P is
       // rounded to bf16 for the second product, as in the other attention
-      // kernels, and turned from rows of keys to columns (the B operand); the
-      // row sum keeps the unrounded values
+      // kernels (V is bf16, and both operands have one type: at most 2^-8 of each weight,
+      // less than the rounding of O itself once a row has a few keys), and turned
+      // from rows of keys to columns (the B operand); the row sum keeps the
+      // unrounded values
       uint32_t pb[NB][MT][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -973,7 +977,8 @@ __global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const AttendParam
   };
   griddep_wait();
 
-  // statistics: thread = (head threadIdx.x % 4, parts threadIdx.x / 4, + 64, ...)
+  // statistics: thread = (head threadIdx.x % kJoinHeads, every (kJoinThreads /
+  // kJoinHeads)-th part from threadIdx.x / kJoinHeads on)
   const int hr = threadIdx.x % kJoinHeads;
   float m = -INFINITY, l = 0.f;
   if (hr < hn)

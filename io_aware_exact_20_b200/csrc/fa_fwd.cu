@@ -16,6 +16,9 @@
 //   P = exp2(S * scale * log2e - m)   online softmax, one thread per row
 //   O_h += P V_h            tcgen05.mma with P read from TMEM
 //
+// P is rounded to bf16 there (V is bf16, and an instruction takes one type for
+// both; at most 2^-8 of each weight); l sums the unrounded values in fp32.
+//
 // and at the end the streams of a Q tile merge: with M = max_h m_h,
 // O = sum_h 2^(m_h - M) O_h / sum_h 2^(m_h - M) l_h (the softmax of a key range
 // split in two, recombined from per-part statistics as in the pages' tiling

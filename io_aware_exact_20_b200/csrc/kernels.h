@@ -13,7 +13,9 @@ namespace fa {
 // Launches `kern` on `stream` with programmatic stream serialization: it may
 // start launching while the previous kernel of the stream finishes its last
 // wave (every kernel of the library waits for its predecessor with
-// griddepcontrol.wait before touching global memory, see ptx.cuh).
+// griddepcontrol.wait before touching global memory, see ptx.cuh; the one
+// exception, decode's join_kernel, reads lengths before it, which needs the
+// kernel in front of it to wait before it releases its dependents).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_overlapped(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t stream, Args&&... args) {

@@ -51,11 +51,14 @@ __device__ __forceinline__ bool elect_one() {
 // have completed and their writes are visible.  A no-op for a normal launch.
 // Every kernel of the library calls it before its first global-memory access,
 // so that launching early only overlaps the launch latency and the CTA
-// rasterisation with the previous kernel's last wave.
+// rasterisation with the previous kernel's last wave.  (decode's join_kernel
+// alone reads what kernels before its predecessor wrote ahead of it.)
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the next kernel in the stream (if launched with programmatic stream
 // serialization) start launching once every CTA of this grid has executed it.
+// A kernel that calls it after its own griddep_wait starts its dependents only
+// when everything before it is done and visible.
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
