@@ -1062,15 +1062,21 @@ Plan plan_of(const Cache& c, int batch, int heads, int window, int sinks) {
   const long long rows = static_cast<long long>(batch) * c.heads_kv * ((G + HB - 1) / HB);
   Plan p;
   p.tiles = rows * (tiles + kRowCost);
-  // A cluster per row where all rows' clusters are resident at once (not every
-  // slot of the GPU can be in a cluster of 8) and a warp's tiles then are at most
-  // four more than in equal shares: the time that joining and working out the
-  // shares take.
+  // A cluster per row where all rows' clusters are resident at once (of clusters
+  // of 8 at one block per SM, 12 are and 16 are not: 7.8 and 14.1 us at d = 256, 512
+  // keys) and the longest row that the table has room for gives a warp at most
+  // four tiles.  A cluster's time is that of its longest row, equal shares' that
+  // of the mean one and 3 us more.  Clusters and shares, d = 128, groups of 4, at 1, 4,
+  // 8 and 32 tiles a warp: 32 sequences over 4 K / V heads, all as long as the
+  // table, 5.7 / 8.9, 9.5 / 11.9, 14.5 / 16.2 and 49 / 51 us; lengths spread over
+  // their logarithm 5.8 / 8.8, 8.8 / 9.9, 13.9 / 10.9 and 41 / 15; one sequence, as
+  // long as the table, 6.6 / 7.4, 9.5 / 9.9, 14.0 / 8.7 and 41 / 13, a quarter of it
+  // 6.3 / 6.9, 6.4 / 7.6, 7.4 / 8.4 and 14 / 8.7.
+  auto resident = [&](int blocks) { return blocks == 8 && per_sm == 1 ? 96ll : 128ll * per_sm; };
   int cs = 8;
-  while (cs > 1 && rows * cs > 128ll * per_sm) cs /= 2;
+  while (cs > 1 && rows * cs > resident(cs)) cs /= 2;
   while (cs > 1 && tiles <= cs / 2 * kWarps) cs /= 2;  // no warps without tiles
-  const long long equal = (p.tiles + 148ll * per_sm * kWarps - 1) / (148ll * per_sm * kWarps);
-  p.cluster = rows * cs <= 128ll * per_sm && (tiles + cs * kWarps - 1) / (cs * kWarps) <= equal + 4 ? cs : 0;
+  p.cluster = rows * cs <= resident(cs) && tiles <= 4ll * cs * kWarps ? cs : 0;
   p.grid = p.cluster > 0                  ? rows * p.cluster
            : p.tiles < 148ll * per_sm ? p.tiles
                                       : 148ll * per_sm;

@@ -171,3 +171,20 @@ def test_rows_cut_in_batches_of_many_chunks(lib, B, Hkv, G, window, sinks):
     assert (o[empty] == 0).all() and (lse[empty] == float("-inf")).all()
     again = cache.attend(0, q, window=window, sinks=sinks)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("B,Hkv,G,d,room", [(1, 4, 4, 128, 2048), (32, 4, 4, 128, 512), (64, 4, 2, 64, 512), (12, 1, 8, 256, 2048),
+                                            (16, 1, 8, 256, 1024), (13, 1, 1, 256, 1024)])
+def test_both_sides_of_the_clusters_rule(lib, B, Hkv, G, d, room):
+    """Tables with just as much room as a cluster per row takes, and one page more:
+    ragged lengths up to the whole table, on both ways."""
+    r = random.Random(B + d)
+    lens = [r.randint(0, room) for _ in range(B - 1)] + [room]
+    q = randn((B, Hkv * G, d), 49)
+    small = filled(lib, lens, 16, Hkv, d, seed=50)
+    for columns in (room // 16, room // 16 + 1):
+        table = torch.full((B, columns), -1, dtype=torch.int32, device="cuda")
+        table[:, :room // 16] = small.table[:, :room // 16]
+        cache = lib.PagedCache(small.k, small.v, table, small.lengths, small.refs)
+        o, lse = cache.attend(0, q)
+        check_attend(cache, 0, q, None, o, lse, d ** -0.5)
