@@ -50,7 +50,11 @@
  *    shared by all (b, h); entry [r][c] == 0 masks every (query, key) pair with
  *    i / 128 == r and j / 128 == c, and such blocks are neither loaded nor
  *    computed.
- *  - All masks combine by logical AND.
+ *  - All masks combine by logical AND.  A masked key of a 128-key tile that any
+ *    row of a 128-row tile sees takes part in the products with weight 0: its
+ *    K and V have to be finite (so rows behind a padded or packed sequence's end
+ *    as well), or what is not a number reaches rows that do not see it.  The
+ *    paged cache's attention reads visible keys alone.
  *  - stream: a cudaStream_t (NULL = the legacy default stream).  Every call is
  *    asynchronous on that stream; nothing is synchronised and nothing printed.
  *  - Ownership: the caller allocates and frees every buffer.  The library
@@ -373,7 +377,8 @@ fa_status_t fa_cache_extend(const fa_cache_t* cache, const int32_t* slots, const
  * [total][heads_kv][d] with element strides of a row and a head (multiples of
  * 8).  cu NULL: one row per entry (total = n); else int32 [n + 1] offsets, rows
  * cu[i] .. cu[i+1]-1.  A position outside the slot's table or without a page is
- * skipped. */
+ * skipped.  A page that several slots hold is written for all of them
+ * (fa_cache_extend gives a slot its own last page before it grows). */
 fa_status_t fa_cache_write(const fa_cache_t* cache, int layer, const void* k, const void* v,
                            int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
                            const int32_t* slots, const int32_t* start, const int32_t* cu, int n,
@@ -417,7 +422,7 @@ fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from,
  * LSE = -inf; what is not a number in a query or a key that it sees makes both
  * none.  heads <= 65535, batch * heads <= 2^31 - 1, and the keys that the
  * batch's rows (one per K / V head and 16 query heads) could see at most, 16 by
- * 16, below 2^32.  workspace: fa_cache_attend_workspace_size bytes (may be 0),
+ * 16 with two such pieces more per row, below 2^32.  workspace: fa_cache_attend_workspace_size bytes (may be 0),
  * 256-byte aligned.  Results repeat to the bit. */
 size_t fa_cache_attend_workspace_size(const fa_cache_t* cache, int batch, int heads, int window,
                                       int sinks);
