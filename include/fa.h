@@ -422,8 +422,9 @@ fa_status_t fa_cache_copy_pages(const fa_cache_t* cache, const fa_cache_t* from,
  * LSE = -inf; what is not a number in a query or a key that it sees makes both
  * none.  heads <= 65535, batch * heads <= 2^31 - 1, and the keys that the
  * batch's rows (one per K / V head and 16 query heads) could see at most, 16 by
- * 16 with two such pieces more per row, below 2^32.  workspace: fa_cache_attend_workspace_size bytes (may be 0),
- * 256-byte aligned.  Results repeat to the bit. */
+ * 16 with two such pieces more per row, below 2^32.  workspace:
+ * fa_cache_attend_workspace_size bytes (may be 0), 256-byte aligned.  Results
+ * repeat to the bit. */
 size_t fa_cache_attend_workspace_size(const fa_cache_t* cache, int batch, int heads, int window,
                                       int sinks);
 fa_status_t fa_cache_attend(const fa_cache_t* cache, int layer, const void* q, void* o, float* lse,

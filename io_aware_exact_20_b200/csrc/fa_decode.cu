@@ -27,8 +27,8 @@
 // Few rows of few tiles, where latency counts, take another way to the same sums:
 // a cluster of up to 8 blocks per row, whose warps take turns, and whose parts
 // meet through the cluster's shared memory: one launch, no shares to work out
-// and nothing to join (one sequence of 500 keys 6.8 us instead of 9.5, 64 of 60 keys 5.6
-// instead of 11.2).
+// and nothing to join (one sequence of 500 keys 6.6 us instead of 7.8, 32 of 64 keys
+// over 8 K / V heads 5.2 instead of 9.4).
 //
 // Visible keys are counted u = 0 .. n_vis - 1: the first `sinks` that the window
 // does not reach, then the window.  A tile is KT consecutive u, each with its

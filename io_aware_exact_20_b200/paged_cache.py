@@ -22,8 +22,8 @@ class PagedCache:
     The tensors stay the caller's (they may be views of one buffer) and are
     changed in place; ``allocate`` makes an empty cache.  The library keeps their
     addresses, so these attributes and the sizes cannot be set: other tensors are
-    another PagedCache.  Slots are given as int32 device
-    tensors.  Calls on one cache have to be ordered: one stream, or events."""
+    another PagedCache.  Slots are given as int32 device tensors.  Calls on one
+    cache have to be ordered: one stream, or events."""
 
     _FIXED = frozenset(("k", "v", "table", "lengths", "refs", "layers", "pages", "heads_kv", "page_size",
                         "head_dim", "slots", "max_pages", "device"))
